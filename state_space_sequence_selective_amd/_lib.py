@@ -1,5 +1,5 @@
 """ctypes binding of libmamba_scan.so (include/mamba_scan.h, include/mamba_layer.h,
-include/mamba3.h).
+include/mamba3.h, include/mamba_gdelta.h, include/mamba_norm.h).
 
 Argument marshalling only: tensors are checked for device, dtype, layout and
 size, their device pointers are handed to the C entry points, and a non-zero
@@ -26,7 +26,9 @@ EXPORTED = ("mamba_abi_version", "mamba_last_error", "mamba_ckpt_bytes", "mamba_
             "mamba_scan_fwd", "mamba_scan_bwd", "mamba_scan_bwd_static", "mamba_conv_scan_gate_fwd",
             "mamba_conv_scan_gate_bwd",
             "mamba_layer_saved_bytes", "mamba_layer_workspace_bytes", "mamba_layer_fwd", "mamba_layer_bwd",
-            "mamba3_states_bytes", "mamba3_workspace_bytes", "mamba3_siso_fwd", "mamba3_siso_bwd")
+            "mamba3_states_bytes", "mamba3_workspace_bytes", "mamba3_siso_fwd", "mamba3_siso_bwd",
+            "mamba_gdelta_saved_bytes", "mamba_gdelta_workspace_bytes", "mamba_gdelta_fwd", "mamba_gdelta_bwd",
+            "mamba_gdelta_step", "mamba_layernorm_workspace_bytes", "mamba_layernorm_fwd", "mamba_layernorm_bwd")
 
 # weights of one layer (mamba_layer_weights_t / mamba_layer_grads_t field order)
 LAYER_PARAMS = ("norm_w", "w_in", "conv_w", "conv_b", "w_x", "w_dt", "b_dt", "a_log", "D", "w_out")
@@ -119,6 +121,23 @@ def load():
     lib.mamba3_siso_fwd.argtypes = [M3] + [P] * 14 + [ctypes.c_size_t, P]
     lib.mamba3_siso_bwd.restype = ctypes.c_int
     lib.mamba3_siso_bwd.argtypes = [M3] + [P] * 25 + [ctypes.c_size_t, P]
+    GD, N = ctypes.POINTER(GDeltaDims), ctypes.c_size_t
+    for name, dims in (("mamba_gdelta_saved_bytes", GD), ("mamba_gdelta_workspace_bytes", GD),
+                       ("mamba_layernorm_workspace_bytes", ctypes.POINTER(NormDims))):
+        f = getattr(lib, name)
+        f.restype = ctypes.c_int
+        f.argtypes = [dims, ctypes.POINTER(N)]
+    lib.mamba_gdelta_fwd.restype = ctypes.c_int
+    lib.mamba_gdelta_fwd.argtypes = [GD] + [P] * 11 + [N, P, N, P]
+    lib.mamba_gdelta_bwd.restype = ctypes.c_int
+    lib.mamba_gdelta_bwd.argtypes = [GD] + [P] * 7 + [ctypes.c_int32, P, N] + [P] * 9 + [N, P]
+    lib.mamba_gdelta_step.restype = ctypes.c_int
+    lib.mamba_gdelta_step.argtypes = [GD] + [P] * 10
+    ND = ctypes.POINTER(NormDims)
+    lib.mamba_layernorm_fwd.restype = ctypes.c_int
+    lib.mamba_layernorm_fwd.argtypes = [ND] + [P] * 7
+    lib.mamba_layernorm_bwd.restype = ctypes.c_int
+    lib.mamba_layernorm_bwd.argtypes = [ND] + [P] * 10 + [N, P]
     _lib = lib
     return lib
 
@@ -445,3 +464,134 @@ def m3_bwd(d: M3Dims, x, b_in, c_in, dd_dt_raw, dd_a_raw, trap_raw, angles_raw, 
              _ptr(d_dt_bias, "d_dt_bias", f, s["h"], True), _ptr(d_D, "d_D", f, s["h"], D is not None),
              *_workspace(workspace), _stream(stream)]
     _check(load().mamba3_siso_bwd(*args))
+
+
+# ----------------------------------------------------- gated delta rule core
+
+
+class GDeltaDims(ctypes.Structure):
+    """mamba_gdelta_dims_t."""
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("groups", ctypes.c_int64), ("d_k", ctypes.c_int64), ("d_v", ctypes.c_int64),
+                ("act", ctypes.c_int32), ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+    @classmethod
+    def make(cls, batch, seqlen, heads, d_k, d_v, groups=None, act="bf16", scale=0.0, eps=1e-6):
+        code = ACT_CODES[act] if isinstance(act, str) else int(act)
+        return cls(batch, seqlen, heads, heads if groups is None else groups, d_k, d_v, code, scale, eps)
+
+    @property
+    def act_dtype(self) -> torch.dtype:
+        return TORCH_DTYPES[self.act]
+
+    def shapes(self) -> dict:
+        B, T, H, G, K, V = self.batch, self.seqlen, self.heads, self.groups, self.d_k, self.d_v
+        return dict(qk=(B, T, G, K), v=(B, T, H, V), gate=(B, T, H), h=(H,), state=(B, H, V, K))
+
+
+class NormDims(ctypes.Structure):
+    """mamba_norm_dims_t."""
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("x", ctypes.c_int32), ("y", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+    @classmethod
+    def make(cls, rows, dim, x="f32", y="bf16", eps=1e-5):
+        code = lambda a: ACT_CODES[a] if isinstance(a, str) else int(a)
+        return cls(rows, dim, code(x), code(y), eps)
+
+    @property
+    def x_dtype(self) -> torch.dtype:
+        return TORCH_DTYPES[self.x]
+
+    @property
+    def y_dtype(self) -> torch.dtype:
+        return TORCH_DTYPES[self.y]
+
+
+def _bytes(fn, d) -> int:
+    out = ctypes.c_size_t(0)
+    _check(getattr(load(), fn)(ctypes.byref(d), ctypes.byref(out)))
+    return out.value
+
+
+def gdelta_saved_bytes(d: GDeltaDims) -> int:
+    return _bytes("mamba_gdelta_saved_bytes", d)
+
+
+def gdelta_workspace_bytes(d: GDeltaDims) -> int:
+    return _bytes("mamba_gdelta_workspace_bytes", d)
+
+
+def _gdelta_shapes(d: GDeltaDims) -> dict:
+    """d.shapes(), cached per distinct dims (a decoding step asks for them on every call)."""
+    key = bytes(d)
+    s = _SHAPES.get(key)
+    if s is None:
+        s = d.shapes()
+        if len(_SHAPES) > 256:
+            _SHAPES.clear()
+        _SHAPES[key] = s
+    return s
+
+
+def _gdelta_inputs(d, s, q, k, v, a_raw, b_raw, a_log, dt_bias):
+    at, f = d.act_dtype, torch.float32
+    return [ctypes.byref(d), _ptr(q, "q", at, s["qk"], True), _ptr(k, "k", at, s["qk"], True),
+            _ptr(v, "v", at, s["v"], True), _ptr(a_raw, "a_raw", f, s["gate"], True),
+            _ptr(b_raw, "b_raw", f, s["gate"], True), _ptr(a_log, "a_log", f, s["h"], True),
+            _ptr(dt_bias, "dt_bias", f, s["h"], True)]
+
+
+def gdelta_fwd(d: GDeltaDims, q, k, v, a_raw, b_raw, a_log, dt_bias, h0=None, *, y, h_last=None, saved=None,
+               workspace=None, stream=None):
+    s, f = _gdelta_shapes(d), torch.float32
+    sp, sn = (None, 0) if saved is None else _buffer(saved, "saved")
+    args = _gdelta_inputs(d, s, q, k, v, a_raw, b_raw, a_log, dt_bias)
+    args += [_ptr(h0, "h0", f, s["state"]), _ptr(y, "y", d.act_dtype, s["v"], True),
+             _ptr(h_last, "h_last", f, s["state"]), sp, sn, *_workspace(workspace), _stream(stream)]
+    _check(load().mamba_gdelta_fwd(*args))
+
+
+def gdelta_bwd(d: GDeltaDims, q, k, v, a_raw, b_raw, a_log, dt_bias, saved, dy, *, d_q, d_k, d_v, d_a_raw, d_b_raw,
+               d_a_log, d_dt_bias, workspace, has_h0=False, stream=None):
+    s, at, f = _gdelta_shapes(d), d.act_dtype, torch.float32
+    args = _gdelta_inputs(d, s, q, k, v, a_raw, b_raw, a_log, dt_bias)
+    args += [int(bool(has_h0)), *_buffer(saved, "saved"), _ptr(dy, "dy", at, s["v"], True),
+             _ptr(d_q, "d_q", at, s["qk"], True), _ptr(d_k, "d_k", at, s["qk"], True),
+             _ptr(d_v, "d_v", at, s["v"], True), _ptr(d_a_raw, "d_a_raw", f, s["gate"], True),
+             _ptr(d_b_raw, "d_b_raw", f, s["gate"], True), _ptr(d_a_log, "d_a_log", f, s["h"], True),
+             _ptr(d_dt_bias, "d_dt_bias", f, s["h"], True), *_buffer(workspace, "workspace"), _stream(stream)]
+    _check(load().mamba_gdelta_bwd(*args))
+
+
+def gdelta_step(d: GDeltaDims, q, k, v, a_raw, b_raw, a_log, dt_bias, state, *, y, stream=None):
+    """The tokens of a decoding step; ``state`` [B, heads, d_v, d_k] f32 is updated in place."""
+    s = _gdelta_shapes(d)
+    args = _gdelta_inputs(d, s, q, k, v, a_raw, b_raw, a_log, dt_bias)
+    args += [_ptr(state, "state", torch.float32, s["state"], True), _ptr(y, "y", d.act_dtype, s["v"], True),
+             _stream(stream)]
+    _check(load().mamba_gdelta_step(*args))
+
+
+# -------------------------------------------------------------- layer norm
+
+
+def layernorm_workspace_bytes(d: NormDims) -> int:
+    return _bytes("mamba_layernorm_workspace_bytes", d)
+
+
+def layernorm_fwd(d: NormDims, x, w=None, b=None, *, y, mean=None, rstd=None, stream=None):
+    f, shape, rows, cols = torch.float32, (d.rows, d.dim), (d.rows,), (d.dim,)
+    _check(load().mamba_layernorm_fwd(ctypes.byref(d), _ptr(x, "x", d.x_dtype, shape, True), _ptr(w, "w", f, cols),
+                                      _ptr(b, "b", f, cols), _ptr(y, "y", d.y_dtype, shape, True),
+                                      _ptr(mean, "mean", f, rows), _ptr(rstd, "rstd", f, rows), _stream(stream)))
+
+
+def layernorm_bwd(d: NormDims, x, w, mean, rstd, dy, d_add=None, *, dx, d_w=None, d_b=None, workspace=None,
+                  stream=None):
+    f, shape, rows, cols = torch.float32, (d.rows, d.dim), (d.rows,), (d.dim,)
+    _check(load().mamba_layernorm_bwd(ctypes.byref(d), _ptr(x, "x", d.x_dtype, shape, True), _ptr(w, "w", f, cols),
+                                      _ptr(mean, "mean", f, rows, True), _ptr(rstd, "rstd", f, rows, True),
+                                      _ptr(dy, "dy", d.y_dtype, shape, True), _ptr(d_add, "d_add", d.x_dtype, shape),
+                                      _ptr(dx, "dx", d.x_dtype, shape, True), _ptr(d_w, "d_w", f, cols),
+                                      _ptr(d_b, "d_b", f, cols), *_workspace(workspace), _stream(stream)))
