@@ -56,7 +56,7 @@ typedef struct {
   int64_t d_k;     /* 8 .. 128, a multiple of 8 */
   int64_t d_v;     /* 8 .. 512, a multiple of 8 */
   int32_t act;     /* mamba_dtype_t of q, k, v, y and their gradients */
-  float scale;     /* of y; 0 = 1 / sqrt(d_k) */
+  float scale;     /* of y, 1e-6 .. 1e6 in size; 0 = 1 / sqrt(d_k) */
   float eps;       /* > 0: added to |q|^2 and |k|^2 */
 } mamba_gdelta_dims_t;
 

@@ -53,7 +53,11 @@ struct Dims {
   int64_t B, T, H, G, nc;   // G: query / key heads
   int K, V, VP;             // d_k, d_v, d_v rounded up to 32
   float scale, eps;
+  float pscale;             // power of two that P = q.k^T D is kept times (|P| <= |scale|)
 };
+
+// T's entries are at most 1: its f16 parts are kept times this, as small ones would lose bits below 2^-24
+constexpr float kTScale = 4096.0f;
 
 // What the chunks keep for each other and for the backward pass, [B * H][nc] outermost
 struct Kept {
@@ -117,6 +121,26 @@ struct Frag {
   h8 hi, lo;
 };
 
+// An address as a wave-uniform base and a 32-bit byte offset of the lane (the saddr form: no 64-bit address registers)
+template <class T>
+__device__ __forceinline__ T& at(void* base, uint32_t off) {
+  return *reinterpret_cast<T*>(static_cast<char*>(base) + off);
+}
+template <class T>
+__device__ __forceinline__ const T& at(const void* base, uint32_t off) {
+  return *reinterpret_cast<const T*>(static_cast<const char*>(base) + off);
+}
+
+// The value, as something the compiler cannot carry out of a loop: multiples of a row length are cheaper to make again
+// than to keep, one pair of scalar registers each
+__device__ __forceinline__ int64_t fresh(int64_t x) {
+  int lo = __builtin_amdgcn_readfirstlane(static_cast<int>(x));
+  asm volatile("" : "+s"(lo));
+  return lo;
+}
+
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // two stacked D tiles as a split B operand
 __device__ __forceinline__ Frag to_b(f32x4 a, f32x4 b) {
   u32x4 hi, lo;
@@ -126,6 +150,19 @@ __device__ __forceinline__ Frag to_b(f32x4 a, f32x4 b) {
   split2(b[0], b[1], x, y); hi[2] = x; lo[2] = y;
   split2(b[2], b[3], x, y); hi[3] = x; lo[3] = y;
   return {__builtin_bit_cast(h8, hi), __builtin_bit_cast(h8, lo)};
+}
+
+// Stores a split operand's parts as f16 high | low << 16 words to its 4 + 4 rows 4 g + e, 16 + 4 g + e of `rows` words;
+// off: the lane's byte offset in the first of them
+__device__ __forceinline__ void store_packed(uint32_t* base, uint32_t off, const Frag& f, int64_t rows_) {
+  const int64_t rows = fresh(rows_);
+  const u32x4 hi = __builtin_bit_cast(u32x4, f.hi), lo = __builtin_bit_cast(u32x4, f.lo);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t* q = base + ((e >> 1) * 16 + (e & 1) * 2) * rows;
+    at<uint32_t>(q, off) = (hi[e] & 0xffffu) | (lo[e] << 16);
+    at<uint32_t>(q + rows, off) = (hi[e] >> 16) | (lo[e] & 0xffff0000u);
+  }
 }
 
 __device__ __forceinline__ h8 ld8(const uint16_t* p) { return *reinterpret_cast<const h8*>(p); }
@@ -204,60 +241,110 @@ template <int KP>
 constexpr int kRow = KP + 8;    // [64][kRow]: token rows, d_k in place() order
 constexpr int kCol = kC + 8;    // [KP][kCol] and [64][kCol]: token columns in place() order
 
-// Stages a [64, d_k] tile of q or k times its per-token power of two: token rows to `rows`, and its transpose to
-// `cols`; a plane of f16, and for f32 input a second one with the remainders.  src points at token 0 of the chunk.
-template <Act A, int KP, bool ROWS, bool COLS>
-__device__ __forceinline__ void stage_tile(const void* src, int64_t base, int64_t stride, int K, int64_t left, const float* pw,
-                                           uint16_t* rows, uint16_t* cols, int tid, int nthreads) {
-  constexpr int NG = KP / 8;
-  constexpr int NP = A == Act::F32 ? 2 : 1;
-  for (int i = tid; i < (kC / 4) * NG; i += nthreads) {
-    const int c = (i % NG) * 8, t = (i / NG) * 4;
-    float x[4][8];
+// A workgroup's share of a chunk's q and k rows on their way from global memory to LDS.  A unit is four token rows by
+// eight columns; k's units come first, then q's, NU of them to each of NT threads.
+template <Act A, int KP, int NT>
+struct QkRegs {
+  static constexpr int NG = KP / 8, UNITS = (kC / 4) * NG, NU = 2 * UNITS / NT;
+  static constexpr int W = A == Act::F32 ? 2 : 1;
+  static_assert(2 * UNITS % NT == 0 && UNITS % 64 == 0, "a wave's units are all of k or all of q");
+  u32x4 x[NU][4][W];
+  f32x4 pw[NU];
+
+  // q, k: element 0 of the chunk's first row of the head; rows `stride` elements apart, `left` of them; K columns
+  __device__ __forceinline__ void load(const void* k, const void* q, int64_t base, int64_t stride, int K, int64_t left,
+                                       const float* sc, int tid) {
+    const int w0 = wave_id() * 64;
+    const bool full = left >= kC && K == KP;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) load8<A>(src, base + (t + r) * stride + c, t + r < left && c < K, x[r]);
+    for (int u = 0; u < NU; ++u) {
+      const int n = (tid + u * NT) % UNITS, c = (n % NG) * 8, t = (n / NG) * 4;
+      const bool isq = w0 + u * NT >= UNITS;
+      const char* src = static_cast<const char*>(isq ? q : k) + base * (W * 2);
+      const uint32_t off = (static_cast<uint32_t>(t) * static_cast<uint32_t>(stride) + c) * (W * 2);
+      pw[u] = at<f32x4>(sc + (isq ? SC_PQ : SC_PK) * kC, t * 4);
+      if (full) {
+        const int64_t row = fresh(stride * (W * 2));
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float s = pw[t + r];
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[r][e] *= s;
+          for (int w = 0; w < W; ++w) x[u][r][w] = at<u32x4>(src + r * row + 16 * w, off);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            x[u][r][w] = u32x4{0u, 0u, 0u, 0u};
+            if (t + r < left && c < K) x[u][r][w] = at<u32x4>(src + r * stride * (W * 2) + 16 * w, off);
+          }
+      }
     }
+  }
+
+  // token rows to `rows` (the other of k's and q's plane sets), their transposes to `cols` (nullptr: not wanted)
+  __device__ __forceinline__ void store(uint16_t* krows, uint16_t* qrows, uint16_t* kcols, uint16_t* qcols, int tid) const {
 #pragma unroll
-    for (int pl = 0; pl < NP; ++pl) {
-      uint32_t w[4][4];   // packed pairs along d_k
+    for (int u = 0; u < NU; ++u) {
+      const int n = (tid + u * NT) % UNITS, c = (n % NG) * 8, t = (n / NG) * 4;
+      const bool isq = wave_id() * 64 + u * NT >= UNITS;
+      uint16_t* rows = isq ? qrows : krows;
+      uint16_t* cols = isq ? qcols : kcols;
+      float f[4][8];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = x[r][2 * e], b = x[r][2 * e + 1];
-          const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
-          w[r][e] = __builtin_bit_cast(uint32_t, h);
-          if (NP == 2 && pl == 0) {
-            x[r][2 * e] = a - static_cast<float>(h[0]);
-            x[r][2 * e + 1] = b - static_cast<float>(h[1]);
+        for (int e = 0; e < 8; ++e) {
+          if constexpr (A == Act::F32) f[r][e] = __builtin_bit_cast(float, static_cast<uint32_t>(x[u][r][e / 4][e % 4]));
+          else f[r][e] = IO<A>::cvt((e & 1) ? x[u][r][0][e / 2] >> 16 : x[u][r][0][e / 2] & 0xffffu);
+          f[r][e] *= pw[u][r];
+        }
+#pragma unroll
+      for (int pl = 0; pl < W; ++pl) {
+        uint32_t w[4][4];   // packed pairs along d_k
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = f[r][2 * e], b = f[r][2 * e + 1];
+            const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
+            w[r][e] = __builtin_bit_cast(uint32_t, h);
+            if (W == 2 && pl == 0) {
+              f[r][2 * e] = a - static_cast<float>(h[0]);
+              f[r][2 * e + 1] = b - static_cast<float>(h[1]);
+            }
+          }
+        if (rows) {
+          uint16_t* p = rows + pl * kC * kRow<KP>;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            *reinterpret_cast<u32x2*>(p + (t + r) * kRow<KP> + place(c)) = u32x2{w[r][0], w[r][1]};
+            *reinterpret_cast<u32x2*>(p + (t + r) * kRow<KP> + place(c + 4)) = u32x2{w[r][2], w[r][3]};
           }
         }
-      if (ROWS) {
-        uint16_t* p = rows + pl * kC * kRow<KP>;
+        if (cols) {
+          uint16_t* p = cols + pl * KP * kCol;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          *reinterpret_cast<u32x2*>(p + (t + r) * kRow<KP> + place(c)) = u32x2{w[r][0], w[r][1]};
-          *reinterpret_cast<u32x2*>(p + (t + r) * kRow<KP> + place(c + 4)) = u32x2{w[r][2], w[r][3]};
-        }
-      }
-      if (COLS) {
-        uint16_t* p = cols + pl * KP * kCol;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t a = w[0][e], b = w[1][e], cc = w[2][e], dd = w[3][e];
-          *reinterpret_cast<u32x2*>(p + (c + 2 * e) * kCol + place(t)) =
-              u32x2{(a & 0xffffu) | (b << 16), (cc & 0xffffu) | (dd << 16)};
-          *reinterpret_cast<u32x2*>(p + (c + 2 * e + 1) * kCol + place(t)) =
-              u32x2{(a >> 16) | (b & 0xffff0000u), (cc >> 16) | (dd & 0xffff0000u)};
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a = w[0][e], b = w[1][e], cc = w[2][e], dd = w[3][e];
+            *reinterpret_cast<u32x2*>(p + (c + 2 * e) * kCol + place(t)) =
+                u32x2{(a & 0xffffu) | (b << 16), (cc & 0xffffu) | (dd << 16)};
+            *reinterpret_cast<u32x2*>(p + (c + 2 * e + 1) * kCol + place(t)) =
+                u32x2{(a >> 16) | (b & 0xffff0000u), (cc >> 16) | (dd & 0xffff0000u)};
+          }
         }
       }
     }
   }
+};
+
+// Stages a chunk's q and k at once (no overlap with anything)
+template <Act A, int KP, int NT>
+__device__ __forceinline__ void stage_qk(const void* k, const void* q, int64_t base, int64_t stride, int K, int64_t left,
+                                         const float* sc, uint16_t* krows, uint16_t* qrows, uint16_t* kcols, uint16_t* qcols,
+                                         int tid) {
+  QkRegs<A, KP, NT> x;
+  x.load(k, q, base, stride, K, left, sc, tid);
+  x.store(krows, qrows, kcols, qcols, tid);
 }
 
 // acc += A-rows (NA planes) times a split B operand: the products that matter at 22 bits

@@ -31,11 +31,14 @@ int check_dims(const mamba_gdelta_dims_t* dd, Dims* d, Act* act) {
   if (dd->d_k < 1 || dd->d_v < 1) return fail(MAMBA_ERR_INVALID, "d_k and d_v must be >= 1");
   if (dd->d_k % 8 != 0 || dd->d_k > 128) return fail(MAMBA_ERR_UNSUPPORTED, "d_k must be a multiple of 8, at most 128");
   if (dd->d_v % 8 != 0 || dd->d_v > 512) return fail(MAMBA_ERR_UNSUPPORTED, "d_v must be a multiple of 8, at most 512");
-  if (!std::isfinite(dd->scale)) return fail(MAMBA_ERR_INVALID, "scale must be finite");
+  if (dd->scale != 0.0f && !(std::fabs(dd->scale) >= 1e-6f && std::fabs(dd->scale) <= 1e6f))
+    return fail(MAMBA_ERR_INVALID, "scale must be 0 (the default) or of a size between 1e-6 and 1e6");
   if (!(dd->eps > 0.0f) || !std::isfinite(dd->eps)) return fail(MAMBA_ERR_INVALID, "eps must be finite and > 0");
   if (dd->seqlen > (int64_t(1) << 24)) return fail(MAMBA_ERR_CAPACITY, "seqlen must be at most 2^24");
   if (dd->batch > (int64_t(1) << 24) || dd->heads > (int64_t(1) << 16))
     return fail(MAMBA_ERR_CAPACITY, "batch must be at most 2^24, heads at most 2^16");
+  if (dd->heads * dd->d_v >= (int64_t(1) << 23) || dd->groups * dd->d_k >= (int64_t(1) << 23))   // 64 rows in 32-bit bytes
+    return fail(MAMBA_ERR_CAPACITY, "heads * d_v and groups * d_k must be below 2^23");
   const int64_t nc = (dd->seqlen + kC - 1) / kC, per = dd->d_v > 32 ? (dd->d_v + 31) / 32 : 1;
   if (dd->batch * dd->heads * (nc > per ? nc : per) >= (int64_t(1) << 24))   // workgroups of 256: fewer than 2^32 threads
     return fail(MAMBA_ERR_CAPACITY, "batch * heads * max(seqlen / 64, d_v / 32) must be below 2^24");
@@ -49,6 +52,9 @@ int check_dims(const mamba_gdelta_dims_t* dd, Dims* d, Act* act) {
   d->VP = (d->V + 31) / 32 * 32;
   d->scale = dd->scale != 0.0f ? dd->scale : 1.0f / std::sqrt(static_cast<float>(dd->d_k));
   d->eps = dd->eps;
+  int e;
+  std::frexp(d->scale, &e);
+  d->pscale = std::ldexp(1.0f, 12 - e);
   *act = static_cast<Act>(dd->act);
   return MAMBA_OK;
 }

@@ -75,17 +75,6 @@ struct BwdLds {
   uint16_t PT[2 * kC * kCol];
 };
 
-// packs a split operand's parts to the f16 high | low << 16 words of its 4 + 4 rows and stores them
-__device__ __forceinline__ void store_packed(uint32_t* dst, const Frag& f, int64_t stride) {
-  const u32x4 hi = __builtin_bit_cast(u32x4, f.hi), lo = __builtin_bit_cast(u32x4, f.lo);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    uint32_t* q = dst + ((e >> 1) * 16 + (e & 1) * 2) * stride;
-    q[0] = (hi[e] & 0xffffu) | (lo[e] << 16);
-    q[stride] = (hi[e] >> 16) | (lo[e] & 0xffff0000u);
-  }
-}
-
 template <Act A, int KP, int NW>
 __global__ void __launch_bounds__(NW * 64) gdelta_bwd_state_kernel(const BwdArgs p) {
   constexpr int NP = A == Act::F32 ? 2 : 1, MT = KP / 16, KS = KP / 32;
@@ -97,7 +86,8 @@ __global__ void __launch_bounds__(NW * 64) gdelta_bwd_state_kernel(const BwdArgs
   const int64_t bh = blockIdx.x / ncb, h = bh % d.H, b = bh / d.H, hk = h / (d.H / d.G);
   const int col = ((blockIdx.x % ncb) * NW + wv) * 16 + r;
   const bool ok = col < d.V, live = col < d.VP;
-  const float so = p.so[bh], rso = 1.0f / so;
+  const float so = p.so[bh], rso = 1.0f / so, rps = 1.0f / d.pscale;
+  const uint32_t poff = (4 * g * d.VP + col) * 4;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   f32x4 dS[MT];
 #pragma unroll
@@ -109,8 +99,7 @@ __global__ void __launch_bounds__(NW * 64) gdelta_bwd_state_kernel(const BwdArgs
     const double Gl = Gs[kC - 1];
     __syncthreads();
     const int64_t qk = ((b * d.T + t0) * d.G + hk) * d.K;
-    stage_tile<A, KP, true, true>(p.k, qk, d.G * d.K, d.K, left, sc + SC_PK * kC, s.k, s.kT, tid, NW * 64);
-    stage_tile<A, KP, true, true>(p.q, qk, d.G * d.K, d.K, left, sc + SC_PQ * kC, s.q, s.qT, tid, NW * 64);
+    stage_qk<A, KP, NW * 64>(p.k, p.q, qk, d.G * d.K, d.K, left, sc, s.k, s.q, s.kT, s.qT, tid);
     __syncthreads();
     // P^T: rows j, columns i; zeros in the tiles below its diagonal that a 32-wide step reads
     for (int i = wv; i < 12; i += NW) {
@@ -129,7 +118,7 @@ __global__ void __launch_bounds__(NW * 64) gdelta_bwd_state_kernel(const BwdArgs
         }
       }
       const int ti = 16 * nt + r;
-      const float rq = sc[SC_RQ * kC + ti];
+      const float rq = sc[SC_RQ * kC + ti] * d.pscale;
       const double Gi = Gs[ti];
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
@@ -154,7 +143,7 @@ __global__ void __launch_bounds__(NW * 64) gdelta_bwd_state_kernel(const BwdArgs
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const Frag f = to_b(dS[2 * ks], dS[2 * ks + 1]);
-      if (live) store_packed(p.DS + (ci * KP + 32 * ks + 4 * g) * d.VP + col, f, d.VP);
+      if (live) store_packed(p.DS + (ci * KP + 32 * ks) * d.VP, poff, f, d.VP);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
         dU[mt] = mma_split<NP>(s.k + (16 * mt + r) * kRow<KP> + 32 * ks + 8 * g, kC * kRow<KP>, f, dU[mt]);
@@ -170,17 +159,21 @@ __global__ void __launch_bounds__(NW * 64) gdelta_bwd_state_kernel(const BwdArgs
       }
     const Frag o0 = to_b(dO[0], dO[1]), o1 = to_b(dO[2], dO[3]);   // 16-bit input: the low parts are zero
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int mt = 0; mt < 4; ++mt) {
+      f32x4 acc = zero;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (mt >= 2 && ks == 0) continue;
         const uint16_t* a = s.PT + (16 * mt + r) * kCol + 32 * ks + 8 * g;
         const Frag& o = ks ? o1 : o0;
         const h8 ah = ld8(a);
-        dU[mt] = mma(ah, o.hi, dU[mt]);
-        dU[mt] = mma(ld8(a + kC * kCol), o.hi, dU[mt]);
-        if (NP == 2) dU[mt] = mma(ah, o.lo, dU[mt]);
+        acc = mma(ah, o.hi, acc);
+        acc = mma(ld8(a + kC * kCol), o.hi, acc);
+        if (NP == 2) acc = mma(ah, o.lo, acc);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dU[mt][e] = fmaf(acc[e], rps, dU[mt][e]);
+    }
     const Frag u0 = to_b(dU[0], dU[1]), u1 = to_b(dU[2], dU[3]);
     f32x4 Y[4] = {zero, zero, zero, zero};
     const uint16_t* T = p.w.TT + ci * (kTFrag * 512) + lane * 8;
@@ -193,9 +186,13 @@ __global__ void __launch_bounds__(NW * 64) gdelta_bwd_state_kernel(const BwdArgs
       a = mma(th, x.lo, a);
       Y[kTTm[f]] = mma(tl, x.hi, a);
     }
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Y[mt][e] *= 1.0f / kTScale;
     if (live) {
-      store_packed(p.DU + (ci * kC + 4 * g) * d.VP + col, to_b(Y[0], Y[1]), d.VP);
-      store_packed(p.DU + (ci * kC + 32 + 4 * g) * d.VP + col, to_b(Y[2], Y[3]), d.VP);
+      store_packed(p.DU + ci * kC * d.VP, poff, to_b(Y[0], Y[1]), d.VP);
+      store_packed(p.DU + (ci * kC + 32) * d.VP, poff, to_b(Y[2], Y[3]), d.VP);
     }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
@@ -366,8 +363,7 @@ __global__ void __launch_bounds__(256) gdelta_bwd_chunk_kernel(const BwdArgs p) 
     }
     __syncthreads();
     if (tid < kC) s.G[tid] = p.w.G[ci * kC + tid];
-    stage_tile<A, KP, true, false>(p.k, qk, d.G * d.K, d.K, left, sc + SC_PK * kC, s.k, nullptr, tid, 256);
-    stage_tile<A, KP, true, false>(p.q, qk, d.G * d.K, d.K, left, sc + SC_PQ * kC, s.q, nullptr, tid, 256);
+    stage_qk<A, KP, 256>(p.k, p.q, qk, d.G * d.K, d.K, left, sc, s.k, s.q, nullptr, nullptr, tid);
     __syncthreads();
     // this wave's columns j of the 64 x 64 gradients
     const int j = 16 * wv + r;
@@ -424,8 +420,7 @@ __global__ void __launch_bounds__(256) gdelta_bwd_chunk_kernel(const BwdArgs p) 
       s.red[4 + wv] = dot;
     }
     __syncthreads();   // k, q read; s.red written
-    stage_tile<A, KP, false, true>(p.k, qk, d.G * d.K, d.K, left, sc + SC_PK * kC, nullptr, s.kT, tid, 256);
-    stage_tile<A, KP, false, true>(p.q, qk, d.G * d.K, d.K, left, sc + SC_PQ * kC, nullptr, s.qT, tid, 256);
+    stage_qk<A, KP, 256>(p.k, p.q, qk, d.G * d.K, d.K, left, sc, nullptr, nullptr, s.kT, s.qT, tid);
     const float sm = pow2_below(fmaxf(fmaxf(s.red[0], s.red[1]), fmaxf(s.red[2], s.red[3])), 13), rsm = 1.0f / sm;
     dot = s.red[4] + s.red[5] + s.red[6] + s.red[7];
 #pragma unroll

@@ -1,6 +1,8 @@
 // Gated delta rule, forward: the per-chunk triangular inverse, the pass over
 // the chunks, and the token-by-token step (gfx950).  The algebra and the
 // number format are in gdelta.h.
+#include <type_traits>
+
 #include "gdelta_launch.h"
 
 namespace gdelta {
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
         v[o] = tr ? (x >= i ? sT[x * kAS + i] : 0.0f) : (x <= i ? sT[i * kAS + x] : 0.0f);
       }
       uint32_t a, bb;
-      split2(v[0], v[1], a, bb);
+      split2(v[0] * kTScale, v[1] * kTScale, a, bb);
       hi[e] = a;
       lo[e] = bb;
     }
@@ -232,8 +234,8 @@ struct FwdLds {
   uint16_t q[NP * kC * kRow<KP>];
   uint16_t kT[NP * KP * kCol];
   uint16_t P[2 * kC * kCol];
-  float beta[kC], ek[kC], eq[kC], dk[kC], rk[kC], rq[kC];
   double G[kC];
+  float beta[kC], ek[kC], eq[kC], dk[kC], rk[kC], rq[kC];
 };
 
 template <Act A, int KP, int NW, bool SAVE>
@@ -242,16 +244,20 @@ __global__ void __launch_bounds__(NW * 64) gdelta_fwd_kernel(const FwdArgs p) {
   __shared__ __attribute__((aligned(16))) FwdLds<A, KP, NW> s;
   static_assert(sizeof(s) <= mscan::kLdsBytes, "LDS");
   const Dims& d = p.d;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, r = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
   const int ncb = (d.VP / 16 + NW - 1) / NW;
   const int64_t bh = blockIdx.x / ncb, h = bh % d.H, b = bh / d.H, hk = h / (d.H / d.G);
   const int col = ((blockIdx.x % ncb) * NW + wv) * 16 + r;
   const bool ok = col < d.V, live = col < d.VP;
+  using Raw = std::conditional_t<A == Act::F32, uint32_t, uint16_t>;
+  constexpr int ES = sizeof(Raw);
+  const uint32_t vrow = static_cast<uint32_t>(d.H) * d.V * ES, vcol = ok ? col : d.V - 1;   // bytes of a token's v; a column to read
+  const uint32_t poff = (4 * g * d.VP + col) * 4;   // this lane's place in the packed S and U
   // the head's power of two: |s|, |v - S k| <= 2 sqrt(T + 1) max(|v|, |h0|) scaled below 2^15
   float m = 0.0f;
   for (int64_t i = lane; i < d.nc; i += 64) m = fmaxf(m, p.w.vmax[bh * d.nc + i]);
   const float sv = pow2_below(wave_max(m), 15 - static_cast<int>(ceilf(1.0f + 0.5f * log2f(static_cast<float>(d.T) + 1.0f))));
-  const float rsv = 1.0f / sv;
+  const float rsv = 1.0f / sv, rps = 1.0f / d.pscale, svc = ok ? sv : 0.0f;
   if (SAVE && tid == 0 && blockIdx.x % ncb == 0) p.w.sv[bh] = sv;
 
   f32x4 S[MT];
@@ -266,27 +272,68 @@ __global__ void __launch_bounds__(NW * 64) gdelta_fwd_kernel(const FwdArgs p) {
     }
   }
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  // what the next chunk reads, in flight while this one computes
+  QkRegs<A, KP, NW * 64> qk;
+  h8 th[6], tl[6];
+  float scal[4];       // beta, e, rk, rq of token `lane`
+  double G, Gl;
+  uint32_t v[4][4];
+  auto load_chunk = [&](int64_t c) {
+    const int64_t t0 = c * kC, ci = bh * d.nc + c;
+    const float* sc = p.w.sc + ci * (kSc * kC);
+    qk.load(p.k, p.q, ((b * d.T + t0) * d.G + hk) * d.K, d.G * d.K, d.K, d.T - t0, sc, tid);
+    G = p.w.G[ci * kC + lane];
+    Gl = p.w.G[ci * kC + kC - 1];
+    scal[0] = sc[SC_BETA * kC + lane];
+    scal[1] = sc[SC_E * kC + lane];
+    scal[2] = sc[SC_RK * kC + lane];
+    scal[3] = sc[SC_RQ * kC + lane];
+  };
+  auto load_t = [&](int64_t c) {
+    const uint16_t* T = p.w.T + (bh * d.nc + c) * (kTFrag * 512);
+#pragma unroll
+    for (int f = 0; f < 6; ++f) {
+      th[f] = at<h8>(T + f * 512, lane * 16);
+      tl[f] = at<h8>(T + (6 + f) * 512, lane * 16);
+    }
+  };
+  auto load_v = [&](int64_t c) {
+    const int64_t left = d.T - c * kC;
+    const char* base = static_cast<const char*>(p.v) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES);
+    const uint32_t off = vrow * 4 * g + vcol * ES;
+    const int64_t row = fresh(vrow);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[mt][e] = 0u;
+        if (left >= kC || 16 * mt + 4 * g + e < left) v[mt][e] = at<Raw>(base + (16 * mt + e) * row, off);
+      }
+  };
+  load_chunk(0);
+  load_t(0);
+  load_v(0);
   for (int64_t c = 0; c < d.nc; ++c) {
     const int64_t t0 = c * kC, left = d.T - t0, ci = bh * d.nc + c;
-    const float* sc = p.w.sc + ci * (kSc * kC);
-    __syncthreads();   // the previous chunk's readers are done
-    if (tid < kC) {
-      const double G = p.w.G[ci * kC + tid], Gl = p.w.G[ci * kC + kC - 1];
-      const float be = sc[SC_BETA * kC + tid], e = sc[SC_E * kC + tid], rk = sc[SC_RK * kC + tid], rq = sc[SC_RQ * kC + tid];
-      s.G[tid] = G;
-      s.beta[tid] = be;
-      s.ek[tid] = e * rk;
-      s.eq[tid] = e * rq;
-      s.dk[tid] = exp2_fast(static_cast<float>(Gl - G)) * rk;
-      s.rk[tid] = rk;
-      s.rq[tid] = rq;
+    mscan::lds_barrier();   // the previous chunk's readers are done
+    qk.store(s.k, s.q, s.kT, nullptr, tid);
+    if (wv == 0) {
+      s.G[lane] = G;
+      s.beta[lane] = scal[0];
+      s.ek[lane] = scal[1] * scal[2];
+      s.eq[lane] = scal[1] * scal[3];
+      s.dk[lane] = exp2_fast(static_cast<float>(Gl - G)) * scal[2];
+      s.rk[lane] = scal[2];
+      s.rq[lane] = scal[3] * d.pscale;
     }
-    const int64_t qk = ((b * d.T + t0) * d.G + hk) * d.K;
-    stage_tile<A, KP, true, true>(p.k, qk, d.G * d.K, d.K, left, sc + SC_PK * kC, s.k, s.kT, tid, NW * 64);
-    stage_tile<A, KP, true, false>(p.q, qk, d.G * d.K, d.K, left, sc + SC_PQ * kC, s.q, nullptr, tid, NW * 64);
-    __syncthreads();
+    const float el = exp2_fast(static_cast<float>(Gl));
+    if (c + 1 < d.nc) load_chunk(c + 1);
+    mscan::lds_barrier();
     // P = q.k^T D on and below the diagonal, zeros in the two tiles above it that a 32-wide step reads
-    for (int i = wv; i < 12; i += NW) {
+#pragma unroll
+    for (int n = 0; n < (12 + NW - 1) / NW; ++n) {
+      const int i = wv + n * NW;
+      if (12 % NW && i >= 12) break;
       const int mt = i < 2 ? 0 : i < 4 ? 1 : i < 8 ? 2 : 3, nt = i - (i < 2 ? 0 : i < 4 ? 2 : i < 8 ? 4 : 8);
       f32x4 acc = zero;
       if (nt <= mt) {
@@ -304,14 +351,14 @@ __global__ void __launch_bounds__(NW * 64) gdelta_fwd_kernel(const FwdArgs p) {
       const int j = 16 * nt + r;
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        float v[2];
+        float x[2];
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
           const int row = 16 * mt + 4 * g + e + o;
-          v[o] = j <= row ? s.rq[row] * s.rk[j] * acc[e + o] * exp2_fast(static_cast<float>(s.G[row] - s.G[j])) : 0.0f;
+          x[o] = j <= row ? s.rq[row] * s.rk[j] * acc[e + o] * exp2_fast(static_cast<float>(s.G[row] - s.G[j])) : 0.0f;
         }
         uint32_t hi, lo;
-        split2(v[0], v[1], hi, lo);
+        split2(x[0], x[1], hi, lo);
         uint16_t* dst = s.P + (16 * mt + 4 * g + e) * kCol + place(j);
         dst[0] = static_cast<uint16_t>(hi);
         dst[kCol] = static_cast<uint16_t>(hi >> 16);
@@ -319,7 +366,6 @@ __global__ void __launch_bounds__(NW * 64) gdelta_fwd_kernel(const FwdArgs p) {
         dst[kC * kCol + kCol] = static_cast<uint16_t>(lo >> 16);
       }
     }
-    __syncthreads();
 
     f32x4 ak[4], aq[4];
 #pragma unroll
@@ -327,16 +373,7 @@ __global__ void __launch_bounds__(NW * 64) gdelta_fwd_kernel(const FwdArgs p) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const Frag f = to_b(S[2 * ks], S[2 * ks + 1]);
-      if (SAVE && live) {
-        const u32x4 hi = __builtin_bit_cast(u32x4, f.hi), lo = __builtin_bit_cast(u32x4, f.lo);
-        uint32_t* dst = p.w.S + (ci * KP + 32 * ks + 4 * g) * d.VP + col;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {   // words: rows 2 e, 2 e + 1 of the 4 + 4 rows 4 g .. and 16 + 4 g ..
-          uint32_t* q = dst + ((e >> 1) * 16 + (e & 1) * 2) * static_cast<int64_t>(d.VP);
-          q[0] = (hi[e] & 0xffffu) | (lo[e] << 16);
-          q[d.VP] = (hi[e] >> 16) | (lo[e] & 0xffff0000u);
-        }
-      }
+      if (SAVE && live) store_packed(p.w.S + (ci * KP + 32 * ks) * d.VP, poff, f, d.VP);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
         const int at = (16 * mt + r) * kRow<KP> + 32 * ks + 8 * g;
@@ -345,56 +382,41 @@ __global__ void __launch_bounds__(NW * 64) gdelta_fwd_kernel(const FwdArgs p) {
       }
     }
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int mt = 0; mt < 4; ++mt) {
+      const f32x4 be = *reinterpret_cast<const f32x4*>(s.beta + 16 * mt + 4 * g), ek = *reinterpret_cast<const f32x4*>(s.ek + 16 * mt + 4 * g);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 16 * mt + 4 * g + e;
-        const float v = ok && t < left ? IO<A>::ld(p.v, ((b * d.T + t0 + t) * d.H + h) * d.V + col) : 0.0f;
-        ak[mt][e] = s.beta[t] * (v * sv - s.ek[t] * ak[mt][e]);
-      }
+      for (int e = 0; e < 4; ++e) ak[mt][e] = be[e] * (IO<A>::cvt(v[mt][e]) * svc - ek[e] * ak[mt][e]);
+    }
     const Frag x0 = to_b(ak[0], ak[1]), x1 = to_b(ak[2], ak[3]);
     f32x4 U[4] = {zero, zero, zero, zero};
-    const uint16_t* T = p.w.T + ci * (kTFrag * 512) + lane * 8;
 #pragma unroll
     for (int f = 0; f < 6; ++f) {
       const Frag& x = kTk[f] ? x1 : x0;
-      const h8 th = ld8(T + f * 512), tl = ld8(T + (6 + f) * 512);
       f32x4 a = U[kTm[f]];
-      a = mma(th, x.hi, a);
-      a = mma(th, x.lo, a);
-      U[kTm[f]] = mma(tl, x.hi, a);
+      a = mma(th[f], x.hi, a);
+      a = mma(th[f], x.lo, a);
+      U[kTm[f]] = mma(tl[f], x.hi, a);
     }
+    if (c + 1 < d.nc) {
+      load_v(c + 1);
+      load_t(c + 1);
+    }
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) U[mt][e] *= 1.0f / kTScale;
     const Frag u0 = to_b(U[0], U[1]), u1 = to_b(U[2], U[3]);
     if (SAVE && live) {
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const Frag& f = ks ? u1 : u0;
-        const u32x4 hi = __builtin_bit_cast(u32x4, f.hi), lo = __builtin_bit_cast(u32x4, f.lo);
-        uint32_t* dst = p.w.U + (ci * kC + 32 * ks + 4 * g) * d.VP + col;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t* q = dst + ((e >> 1) * 16 + (e & 1) * 2) * static_cast<int64_t>(d.VP);
-          q[0] = (hi[e] & 0xffffu) | (lo[e] << 16);
-          q[d.VP] = (hi[e] >> 16) | (lo[e] & 0xffff0000u);
-        }
-      }
+      store_packed(p.w.U + ci * kC * d.VP, poff, u0, d.VP);
+      store_packed(p.w.U + (ci * kC + 32) * d.VP, poff, u1, d.VP);
     }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      f32x4 a = zero;
-      a = mma_split<2>(s.P + (16 * mt + r) * kCol + 8 * g, kC * kCol, u0, a);
-      if (mt >= 2) a = mma_split<2>(s.P + (16 * mt + r) * kCol + 32 + 8 * g, kC * kCol, u1, a);
+      const f32x4 dk = *reinterpret_cast<const f32x4*>(s.dk + 16 * mt + 4 * g);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 16 * mt + 4 * g + e;
-        if (ok && t < left)
-          IO<A>::st(p.y, ((b * d.T + t0 + t) * d.H + h) * d.V + col, (s.eq[t] * aq[mt][e] + a[e]) * rsv);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) U[mt][e] *= s.dk[16 * mt + 4 * g + e];
+      for (int e = 0; e < 4; ++e) U[mt][e] *= dk[e];
     }
     const Frag d0 = to_b(U[0], U[1]), d1 = to_b(U[2], U[3]);
-    const float el = exp2_fast(static_cast<float>(s.G[kC - 1]));
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -402,6 +424,21 @@ __global__ void __launch_bounds__(NW * 64) gdelta_fwd_kernel(const FwdArgs p) {
       const uint16_t* a = s.kT + (16 * mt + r) * kCol + 8 * g;
       S[mt] = mma_split<NP>(a, KP * kCol, d0, S[mt]);
       S[mt] = mma_split<NP>(a + 32, KP * kCol, d1, S[mt]);
+    }
+    mscan::lds_barrier();   // all of P
+    char* y = static_cast<char*>(p.y) + ((b * d.T + t0) * d.H + h) * (d.V * ES);
+    const uint32_t yoff = vrow * 4 * g + col * ES;
+    const int64_t yrow = fresh(vrow);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      f32x4 a = zero;
+      a = mma_split<2>(s.P + (16 * mt + r) * kCol + 8 * g, kC * kCol, u0, a);
+      if (mt >= 2) a = mma_split<2>(s.P + (16 * mt + r) * kCol + 32 + 8 * g, kC * kCol, u1, a);
+      const f32x4 eq = *reinterpret_cast<const f32x4*>(s.eq + 16 * mt + 4 * g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (ok && (left >= kC || 16 * mt + 4 * g + e < left))
+          IO<A>::st(&at<char>(y + (16 * mt + e) * yrow, yoff), 0, (eq[e] * aq[mt][e] + a[e] * rps) * rsv);
     }
   }
   if (p.h_last && ok) {

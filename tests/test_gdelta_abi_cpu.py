@@ -28,9 +28,11 @@ def ln(pkg, **kw):
     (dict(groups=0), 1, "groups"), (dict(heads=5), 1, "multiple of groups"), (dict(act=3), 1, "act"),
     (dict(act=-1), 1, "act"), (dict(d_k=0), 1, "d_k"), (dict(d_v=-8), 1, "d_v"), (dict(d_k=12), 2, "d_k"),
     (dict(d_k=136), 2, "d_k"), (dict(d_v=12), 2, "d_v"), (dict(d_v=520), 2, "d_v"),
-    (dict(scale=float("nan")), 1, "scale"), (dict(scale=float("inf")), 1, "scale"), (dict(eps=0.0), 1, "eps"),
+    (dict(scale=float("nan")), 1, "scale"), (dict(scale=float("inf")), 1, "scale"),
+    (dict(scale=1e-7), 1, "scale"), (dict(scale=-2e6), 1, "scale"), (dict(eps=0.0), 1, "eps"),
     (dict(eps=float("nan")), 1, "eps"), (dict(seqlen=(1 << 24) + 1), 3, "seqlen"),
-    (dict(batch=1 << 25), 3, "batch"), (dict(batch=1 << 20, heads=16), 3, "2^24"),
+    (dict(batch=1 << 25), 3, "batch"),
+    (dict(heads=1 << 15, d_v=512), 3, "heads"), (dict(batch=1 << 20, heads=16), 3, "2^24"),
 ])
 def test_gdelta_dims(pkg, kw, status, msg):
     for f in (pkg.gdelta_saved_bytes, pkg.gdelta_workspace_bytes):
