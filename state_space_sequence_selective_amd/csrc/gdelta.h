@@ -41,13 +41,13 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kC = 64;          // tokens per chunk
-constexpr int kSc = 6;          // per-token scalars kept per chunk: see below
-constexpr int kTFrag = 12;      // 1 KB fragments of T (6 of its 8 row tile / k step pairs, high and low parts)
+constexpr int kFrag = 512;      // u16 of one operand fragment: 64 lanes x 8
 
-// rows of the per-chunk scalar block sc[kSc][64]
-enum { SC_BETA = 0, SC_PK = 1, SC_RK = 2, SC_PQ = 3, SC_RQ = 4, SC_E = 5 };
-// k' = k * pk is what the products take, and k' * rk the unit-length key; q' = q * pq, and q' * rq the unit-length
-// query times the scale; e = exp(G)
+// per-token scalars of a chunk, per query / key head: k' = k pk is what the products take, k' rk the unit-length key;
+// q' = q pq, and q' rq the unit-length query times the scale
+enum { G_PK = 0, G_RK, G_PQ, G_RQ, kGroupSc };
+// and per head: beta, e = exp(G), beta e rk, exp(G_63 - G) rk, e rq
+enum { H_BETA = 0, H_E, H_BK, H_DK, H_EQ, kHeadSc };
 
 struct Dims {
   int64_t B, T, H, G, nc;   // G: query / key heads
@@ -59,16 +59,32 @@ struct Dims {
 // T's entries are at most 1: its f16 parts are kept times this, as small ones would lose bits below 2^-24
 constexpr float kTScale = 4096.0f;
 
-// What the chunks keep for each other and for the backward pass, [B * H][nc] outermost
+// The (row tile, 32-column step) pairs of a lower triangular 64 x 64 matrix that hold anything but zeros, and those of
+// its transpose: six fragments each
+__device__ constexpr int kLm[6] = {0, 1, 2, 2, 3, 3}, kLk[6] = {0, 0, 0, 1, 0, 1};
+__device__ constexpr int kUm[6] = {0, 0, 1, 1, 2, 3}, kUk[6] = {0, 1, 0, 1, 1, 1};
+
+// What the kernels keep for each other.  Fragments are stored as a wave reads them: 1 KB, 16 bytes a lane, lane
+// (r = l % 16, g = l / 16) holding elements (r, place order 8 g ..) of the operand, so the readers need neither LDS
+// nor any rearranging.  f32 inputs have a second plane of every k and q family, with the low parts.
 struct Kept {
-  float* sc;        // [6][64]
+  // [B * G][nc] outermost
+  float* gsc;       // [kGroupSc][64]
+  uint16_t* KF;     // [planes][4 token tiles][KP / 32] k', contracted over d_k
+  uint16_t* KT;     // [planes][KP / 16][2] its transpose, contracted over tokens
+  uint16_t* QF;     // the same of q'
+  uint16_t* QT;     // only for a backward pass
+  // [B * H][nc] outermost
+  float* hsc;       // [kHeadSc][64]
   double* G;        // [64] log2 of the decay since the chunk's start
-  uint16_t* T;      // [12][64][8] f16: T's fragments, high then low parts
-  uint16_t* TT;     // the same of T^T
+  uint16_t* P;      // [1 for bf16, else 2][6] lower triangle of q.k^T D, times pscale
+  uint16_t* PT;     // [2][6] its transpose (backward)
+  uint16_t* T;      // [2][6] the inverse, times kTScale
+  uint16_t* TT;     // [2][6] its transpose (backward)
   float* vmax;      // largest finite |v| of the chunk (the first chunk's entry also holds the initial state's bound)
   float* sv;        // [B * H] the head's power of two for S and u
-  uint32_t* S;      // [KP][VP] the state entering the chunk, f16 high | low << 16, times sv
-  uint32_t* U;      // [64][VP] u, the same
+  uint32_t* S;      // [KP][VP] the state entering the chunk, f16 high | low << 16, times sv (backward)
+  uint32_t* U;      // [64][VP] u, the same (backward)
 };
 
 struct FwdArgs {
@@ -82,8 +98,8 @@ struct FwdArgs {
 
 struct BwdArgs {
   Dims d;
-  const void *q, *k, *v, *dy;
-  const float *a_raw, *b_raw, *a_log, *dt_bias;
+  const void *dy;
+  const float *a_raw, *a_log, *dt_bias;
   bool has_h0;
   Kept w;
   float* dymax;     // [B * H][nc]
@@ -110,11 +126,14 @@ __device__ __forceinline__ constexpr int place(int x) {
   return (x & ~31) + ((x & 15) >> 2) * 8 + ((x >> 4) & 1) * 4 + (x & 3);
 }
 
-// f32 pair -> packed f16 high parts and packed f16 remainders (towards zero: the remainder is exact in f32)
+// f32 pair -> packed f16 high parts and packed f16 remainders, both rounded to nearest (v_cvt_pk_f16_f32; the remainder
+// is exact in f32)
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
+  const h2 h = __builtin_convertvector((f32x2{a, b}), h2);
   hi = __builtin_bit_cast(uint32_t, h);
-  lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a - static_cast<float>(h[0]), b - static_cast<float>(h[1])));
+  lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a - static_cast<float>(h[0]), b - static_cast<float>(h[1])}), h2));
 }
 
 struct Frag {
@@ -236,126 +255,34 @@ __device__ __forceinline__ float log2_decay(float rate, float a_raw, float dt_bi
 // the scale of a row with largest element m and sum of squares ss of the SCALED row (eps scaled along)
 __device__ __forceinline__ float unit_scale(float ss, float p, float eps) { return 1.0f / sqrtf(ss + eps * p * p); }
 
-// LDS planes of one chunk: rows of KP (or 64) f16, 16 bytes of padding against bank conflicts
-template <int KP>
-constexpr int kRow = KP + 8;    // [64][kRow]: token rows, d_k in place() order
-constexpr int kCol = kC + 8;    // [KP][kCol] and [64][kCol]: token columns in place() order
+constexpr int kCol = kC + 8;    // row length of a 64 x 64 f16 plane in LDS: 16 bytes of padding against bank conflicts
 
-// A workgroup's share of a chunk's q and k rows on their way from global memory to LDS.  A unit is four token rows by
-// eight columns; k's units come first, then q's, NU of them to each of NT threads.
-template <Act A, int KP, int NT>
-struct QkRegs {
-  static constexpr int NG = KP / 8, UNITS = (kC / 4) * NG, NU = 2 * UNITS / NT;
-  static constexpr int W = A == Act::F32 ? 2 : 1;
-  static_assert(2 * UNITS % NT == 0 && UNITS % 64 == 0, "a wave's units are all of k or all of q");
-  u32x4 x[NU][4][W];
-  f32x4 pw[NU];
-
-  // q, k: element 0 of the chunk's first row of the head; rows `stride` elements apart, `left` of them; K columns
-  __device__ __forceinline__ void load(const void* k, const void* q, int64_t base, int64_t stride, int K, int64_t left,
-                                       const float* sc, int tid) {
-    const int w0 = wave_id() * 64;
-    const bool full = left >= kC && K == KP;
+// rows times columns of two fragment rows (KS steps, NP planes NF fragments apart)
+template <int NP, int KS, int NF>
+__device__ __forceinline__ f32x4 frag_mm(const uint16_t* a, const uint16_t* b, int lane, f32x4 acc) {
 #pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      const int n = (tid + u * NT) % UNITS, c = (n % NG) * 8, t = (n / NG) * 4;
-      const bool isq = w0 + u * NT >= UNITS;
-      const char* src = static_cast<const char*>(isq ? q : k) + base * (W * 2);
-      const uint32_t off = (static_cast<uint32_t>(t) * static_cast<uint32_t>(stride) + c) * (W * 2);
-      pw[u] = at<f32x4>(sc + (isq ? SC_PQ : SC_PK) * kC, t * 4);
-      if (full) {
-        const int64_t row = fresh(stride * (W * 2));
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int w = 0; w < W; ++w) x[u][r][w] = at<u32x4>(src + r * row + 16 * w, off);
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            x[u][r][w] = u32x4{0u, 0u, 0u, 0u};
-            if (t + r < left && c < K) x[u][r][w] = at<u32x4>(src + r * stride * (W * 2) + 16 * w, off);
-          }
-      }
+  for (int ks = 0; ks < KS; ++ks) {
+    const h8 x = at<h8>(a + ks * kFrag, lane * 16), y = at<h8>(b + ks * kFrag, lane * 16);
+    acc = mma(x, y, acc);
+    if (NP == 2) {
+      acc = mma(x, at<h8>(b + (NF + ks) * kFrag, lane * 16), acc);
+      acc = mma(at<h8>(a + (NF + ks) * kFrag, lane * 16), y, acc);
     }
   }
-
-  // token rows to `rows` (the other of k's and q's plane sets), their transposes to `cols` (nullptr: not wanted)
-  __device__ __forceinline__ void store(uint16_t* krows, uint16_t* qrows, uint16_t* kcols, uint16_t* qcols, int tid) const {
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      const int n = (tid + u * NT) % UNITS, c = (n % NG) * 8, t = (n / NG) * 4;
-      const bool isq = wave_id() * 64 + u * NT >= UNITS;
-      uint16_t* rows = isq ? qrows : krows;
-      uint16_t* cols = isq ? qcols : kcols;
-      float f[4][8];
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if constexpr (A == Act::F32) f[r][e] = __builtin_bit_cast(float, static_cast<uint32_t>(x[u][r][e / 4][e % 4]));
-          else f[r][e] = IO<A>::cvt((e & 1) ? x[u][r][0][e / 2] >> 16 : x[u][r][0][e / 2] & 0xffffu);
-          f[r][e] *= pw[u][r];
-        }
-#pragma unroll
-      for (int pl = 0; pl < W; ++pl) {
-        uint32_t w[4][4];   // packed pairs along d_k
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = f[r][2 * e], b = f[r][2 * e + 1];
-            const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
-            w[r][e] = __builtin_bit_cast(uint32_t, h);
-            if (W == 2 && pl == 0) {
-              f[r][2 * e] = a - static_cast<float>(h[0]);
-              f[r][2 * e + 1] = b - static_cast<float>(h[1]);
-            }
-          }
-        if (rows) {
-          uint16_t* p = rows + pl * kC * kRow<KP>;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            *reinterpret_cast<u32x2*>(p + (t + r) * kRow<KP> + place(c)) = u32x2{w[r][0], w[r][1]};
-            *reinterpret_cast<u32x2*>(p + (t + r) * kRow<KP> + place(c + 4)) = u32x2{w[r][2], w[r][3]};
-          }
-        }
-        if (cols) {
-          uint16_t* p = cols + pl * KP * kCol;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t a = w[0][e], b = w[1][e], cc = w[2][e], dd = w[3][e];
-            *reinterpret_cast<u32x2*>(p + (c + 2 * e) * kCol + place(t)) =
-                u32x2{(a & 0xffffu) | (b << 16), (cc & 0xffffu) | (dd << 16)};
-            *reinterpret_cast<u32x2*>(p + (c + 2 * e + 1) * kCol + place(t)) =
-                u32x2{(a >> 16) | (b & 0xffff0000u), (cc >> 16) | (dd & 0xffff0000u)};
-          }
-        }
-      }
-    }
-  }
-};
-
-// Stages a chunk's q and k at once (no overlap with anything)
-template <Act A, int KP, int NT>
-__device__ __forceinline__ void stage_qk(const void* k, const void* q, int64_t base, int64_t stride, int K, int64_t left,
-                                         const float* sc, uint16_t* krows, uint16_t* qrows, uint16_t* kcols, uint16_t* qcols,
-                                         int tid) {
-  QkRegs<A, KP, NT> x;
-  x.load(k, q, base, stride, K, left, sc, tid);
-  x.store(krows, qrows, kcols, qcols, tid);
-}
-
-// acc += A-rows (NA planes) times a split B operand: the products that matter at 22 bits
-template <int NA>
-__device__ __forceinline__ f32x4 mma_split(const uint16_t* a, int plane, const Frag& b, f32x4 acc) {
-  const h8 ah = ld8(a);
-  acc = mma(ah, b.hi, acc);
-  acc = mma(ah, b.lo, acc);
-  if (NA == 2) acc = mma(ld8(a + plane), b.hi, acc);
   return acc;
 }
 
+// Workgroup n of `per` for each of `heads` heads -> (head, index): workgroups go to the eight XCDs (each with its own
+// L2) in turn, so a head's are given numbers of one XCD, which then reads the head's operands from HBM once
+__device__ __forceinline__ void xcd_head(int64_t n, int per, int64_t heads, int64_t& head, int& idx) {
+  if (heads % 8 == 0) {
+    const int64_t m = n >> 3;
+    head = (m / per) * 8 + (n & 7);
+    idx = static_cast<int>(m % per);
+  } else {
+    head = n / per;
+    idx = static_cast<int>(n % per);
+  }
+}
 
 }  // namespace gdelta

@@ -39,7 +39,7 @@ int check_dims(const mamba_gdelta_dims_t* dd, Dims* d, Act* act) {
     return fail(MAMBA_ERR_CAPACITY, "batch must be at most 2^24, heads at most 2^16");
   if (dd->heads * dd->d_v >= (int64_t(1) << 23) || dd->groups * dd->d_k >= (int64_t(1) << 23))   // 64 rows in 32-bit bytes
     return fail(MAMBA_ERR_CAPACITY, "heads * d_v and groups * d_k must be below 2^23");
-  const int64_t nc = (dd->seqlen + kC - 1) / kC, per = dd->d_v > 32 ? (dd->d_v + 31) / 32 : 1;
+  const int64_t nc = (dd->seqlen + kC - 1) / kC, per = (dd->d_v + 31) / 32;
   if (dd->batch * dd->heads * (nc > per ? nc : per) >= (int64_t(1) << 24))   // workgroups of 256: fewer than 2^32 threads
     return fail(MAMBA_ERR_CAPACITY, "batch * heads * max(seqlen / 64, d_v / 32) must be below 2^24");
   d->B = dd->batch;
@@ -88,18 +88,26 @@ struct Taker {
   }
 };
 
-// [sc | G | T | vmax | sv] and, for a backward pass, [TT | S | U]
-size_t layout_kept(const Dims& d, bool save, char* base, Kept* w) {
-  const size_t chunks = d.B * d.H * d.nc, kp = d.K <= 64 ? 64 : 128;
+// k and q as operands, the chunks' scalars, P and T; and what only a backward pass reads
+size_t layout_kept(const Dims& d, Act act, bool save, char* base, Kept* w) {
+  const size_t chunks = d.B * d.H * d.nc, groups = d.B * d.G * d.nc, kp = d.K <= 64 ? 64 : 128;
+  const size_t planes = act == Act::F32 ? 2 : 1, fam = groups * planes * (kp / 8) * kFrag * 2, tri = chunks * 6 * kFrag * 2;
   Taker t{base};
   *w = Kept{};
-  t.take(w->sc, chunks * kSc * kC * 4);
+  t.take(w->gsc, groups * kGroupSc * kC * 4);
+  t.take(w->KF, fam);
+  t.take(w->KT, fam);
+  t.take(w->QF, fam);
+  t.take(w->hsc, chunks * kHeadSc * kC * 4);
   t.take(w->G, chunks * kC * 8);
-  t.take(w->T, chunks * kTFrag * 1024);
+  t.take(w->P, (act == Act::BF16 ? 1 : 2) * tri);
+  t.take(w->T, 2 * tri);
   t.take(w->vmax, chunks * 4);
   t.take(w->sv, d.B * d.H * 4);
   if (save) {
-    t.take(w->TT, chunks * kTFrag * 1024);
+    t.take(w->QT, fam);
+    t.take(w->PT, 2 * tri);
+    t.take(w->TT, 2 * tri);
     t.take(w->S, chunks * kp * d.VP * 4);
     t.take(w->U, chunks * kC * d.VP * 4);
   }
@@ -148,7 +156,7 @@ int mamba_gdelta_saved_bytes(const mamba_gdelta_dims_t* dims, size_t* bytes) {
   GD_TRY(check_dims(dims, &d, &act));
   if (!bytes) return fail(MAMBA_ERR_INVALID, "bytes is NULL");
   Kept w;
-  *bytes = layout_kept(d, true, nullptr, &w);
+  *bytes = layout_kept(d, act, true, nullptr, &w);
   mscan::set_last_error("");
   return MAMBA_OK;
 }
@@ -161,7 +169,7 @@ int mamba_gdelta_workspace_bytes(const mamba_gdelta_dims_t* dims, size_t* bytes)
   if (!bytes) return fail(MAMBA_ERR_INVALID, "bytes is NULL");
   Kept w;
   BwdArgs a{};
-  const size_t f = layout_kept(d, false, nullptr, &w), b = layout_bwd(d, nullptr, &a);
+  const size_t f = layout_kept(d, act, false, nullptr, &w), b = layout_bwd(d, nullptr, &a);
   *bytes = f > b ? f : b;
   mscan::set_last_error("");
   return MAMBA_OK;
@@ -193,12 +201,12 @@ int mamba_gdelta_fwd(const mamba_gdelta_dims_t* dims, const void* q, const void*
   a.h_last = h_last;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (saved) {
-    GD_TRY(need("saved_bytes", saved_bytes, layout_kept(a.d, true, static_cast<char*>(saved), &a.w)));
+    GD_TRY(need("saved_bytes", saved_bytes, layout_kept(a.d, act, true, static_cast<char*>(saved), &a.w)));
     GD_HIP(launch_fwd(act, a, true, st));
   } else if (a.d.T <= kStepMaxT) {
     GD_HIP(launch_step(act, a, st));
   } else {
-    GD_TRY(need("workspace_bytes", workspace_bytes, layout_kept(a.d, false, static_cast<char*>(workspace), &a.w)));
+    GD_TRY(need("workspace_bytes", workspace_bytes, layout_kept(a.d, act, false, static_cast<char*>(workspace), &a.w)));
     GD_HIP(launch_fwd(act, a, false, st));
   }
   mscan::set_last_error("");
@@ -226,14 +234,10 @@ int mamba_gdelta_bwd(const mamba_gdelta_dims_t* dims, const void* q, const void*
   GD_TRY(check_ptr("d_dt_bias", d_dt_bias, true, 4));
   GD_TRY(check_ptr("workspace", workspace, true, 256));
   GD_TRY(need("saved_bytes", saved_bytes,
-              layout_kept(a.d, true, const_cast<char*>(static_cast<const char*>(saved)), &a.w)));
+              layout_kept(a.d, act, true, const_cast<char*>(static_cast<const char*>(saved)), &a.w)));
   GD_TRY(need("workspace_bytes", workspace_bytes, layout_bwd(a.d, static_cast<char*>(workspace), &a)));
-  a.q = q;
-  a.k = k;
-  a.v = v;
   a.dy = dy;
   a.a_raw = a_raw;
-  a.b_raw = b_raw;
   a.a_log = a_log;
   a.dt_bias = dt_bias;
   a.has_h0 = has_h0 != 0;

@@ -13,6 +13,8 @@
 //   E_ij = dP_ij P_ij + dA_ij A_ij (j < i)
 //   dG_i = sum_j E_ij - sum_j E_ji + q_i.(e dO S^T)_i - k_i.(e beta Y S^T)_i - k_i.(.. U dS'^T)_i
 //   dg_t = sum_{i >= t} dG_i + sum_i k_i.(.. U dS'^T)_i + e_63 <dS', S>
+#include <type_traits>
+
 #include "gdelta_launch.h"
 
 namespace gdelta {
@@ -49,7 +51,7 @@ __global__ void __launch_bounds__(64) gdelta_dscale_kernel(const BwdArgs p) {
     const int64_t c = c0 + lane, ci = bh * d.nc + c;
     const bool ok = c < d.nc;
     const float m = ok ? p.dymax[ci] : 0.0f;
-    const float e = ok ? p.w.sc[ci * (kSc * kC) + SC_E * kC + kC - 1] : 1.0f;
+    const float e = ok ? p.w.hsc[ci * (kHeadSc * kC) + H_E * kC + kC - 1] : 1.0f;
     const float add = static_cast<float>(kC) * fabsf(d.scale) * m;
     top = fmaxf(top, m);
     for (int i = 63; i >= 0; --i) {
@@ -63,193 +65,231 @@ __global__ void __launch_bounds__(64) gdelta_dscale_kernel(const BwdArgs p) {
 }
 
 // ------------------------------------------------------------------ pass from the last chunk to the first
-__device__ constexpr int kTTm[6] = {0, 0, 1, 1, 2, 3}, kTTk[6] = {0, 1, 0, 1, 1, 1};
-
+// As the forward's pass: a wave holds 16 columns of dS^T and needs nothing of any other.
 template <Act A, int KP>
-struct BwdLds {
-  static constexpr int NP = A == Act::F32 ? 2 : 1;
-  uint16_t k[NP * kC * kRow<KP>];
-  uint16_t q[NP * kC * kRow<KP>];
-  uint16_t kT[NP * KP * kCol];
-  uint16_t qT[NP * KP * kCol];
-  uint16_t PT[2 * kC * kCol];
-};
-
-template <Act A, int KP, int NW>
-__global__ void __launch_bounds__(NW * 64) gdelta_bwd_state_kernel(const BwdArgs p) {
-  constexpr int NP = A == Act::F32 ? 2 : 1, MT = KP / 16, KS = KP / 32;
-  __shared__ __attribute__((aligned(16))) BwdLds<A, KP> s;
-  static_assert(sizeof(s) <= mscan::kLdsBytes, "LDS");
+__global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
+  constexpr int NP = A == Act::F32 ? 2 : 1, MT = KP / 16, KS = KP / 32, NF = KP / 8;
+  constexpr bool AHEAD = NP == 1;
+  using Raw = std::conditional_t<A == Act::F32, uint32_t, uint16_t>;
+  constexpr int ES = sizeof(Raw);
+  __shared__ __attribute__((aligned(16))) float s[4][kC];   // beta; beta e rk; exp(G_63 - G) rk; e rq
   const Dims& d = p.d;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, r = lane & 15, g = lane >> 4;
-  const int ncb = (d.VP / 16 + NW - 1) / NW;
-  const int64_t bh = blockIdx.x / ncb, h = bh % d.H, b = bh / d.H, hk = h / (d.H / d.G);
-  const int col = ((blockIdx.x % ncb) * NW + wv) * 16 + r;
-  const bool ok = col < d.V, live = col < d.VP;
-  const float so = p.so[bh], rso = 1.0f / so, rps = 1.0f / d.pscale;
+  const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
+  int64_t bh;
+  int cb;
+  xcd_head(blockIdx.x, d.VP / 16, d.B * d.H, bh, cb);
+  const int64_t h = bh % d.H, b = bh / d.H, bg = b * d.G + h / (d.H / d.G);
+  const int col = cb * 16 + r;
+  const bool ok = col < d.V;
+  const uint32_t vrow = static_cast<uint32_t>(d.H) * d.V * ES;
+  const uint32_t voff = vrow * 4 * g + (ok ? col : d.V - 1) * ES, yoff = vrow * 4 * g + col * ES;
   const uint32_t poff = (4 * g * d.VP + col) * 4;
+  const float so = p.so[bh], rso = 1.0f / so, rps = 1.0f / d.pscale, soc = ok ? so : 0.0f;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   f32x4 dS[MT];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) dS[mt] = zero;
-  for (int64_t c = d.nc - 1; c >= 0; --c) {
-    const int64_t t0 = c * kC, left = d.T - t0, ci = bh * d.nc + c;
-    const float* sc = p.w.sc + ci * (kSc * kC);
-    const double* Gs = p.w.G + ci * kC;
-    const double Gl = Gs[kC - 1];
-    __syncthreads();
-    const int64_t qk = ((b * d.T + t0) * d.G + hk) * d.K;
-    stage_qk<A, KP, NW * 64>(p.k, p.q, qk, d.G * d.K, d.K, left, sc, s.k, s.q, s.kT, s.qT, tid);
-    __syncthreads();
-    // P^T: rows j, columns i; zeros in the tiles below its diagonal that a 32-wide step reads
-    for (int i = wv; i < 12; i += NW) {
-      const int mt = i < 4 ? 0 : i < 8 ? 1 : i < 10 ? 2 : 3, nt = i < 8 ? (i & 3) : 2 + (i & 1);
-      f32x4 acc = zero;
-      if (nt >= mt) {
+  h8 kf[NF], kt[NF], qt[NF], ph[6], pl[6], th[6], tl[6];
+  float sc[4], el;
+  uint32_t v[4][4];
+  auto frags = [&](h8* x, const uint16_t* base, int n) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint16_t* pa = s.k + (16 * mt + r) * kRow<KP> + 32 * ks + 8 * g;
-          const uint16_t* pb = s.q + (16 * nt + r) * kRow<KP> + 32 * ks + 8 * g;
-          acc = mma(ld8(pa), ld8(pb), acc);
-          if (NP == 2) {
-            acc = mma(ld8(pa), ld8(pb + kC * kRow<KP>), acc);
-            acc = mma(ld8(pa + kC * kRow<KP>), ld8(pb), acc);
-          }
-        }
-      }
-      const int ti = 16 * nt + r;
-      const float rq = sc[SC_RQ * kC + ti] * d.pscale;
-      const double Gi = Gs[ti];
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        float v[2];
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          const int tj = 16 * mt + 4 * g + e + o;
-          v[o] = tj <= ti ? rq * sc[SC_RK * kC + tj] * acc[e + o] * exp2_fast(static_cast<float>(Gi - Gs[tj])) : 0.0f;
-        }
-        uint32_t hi, lo;
-        split2(v[0], v[1], hi, lo);
-        uint16_t* dst = s.PT + (16 * mt + 4 * g + e) * kCol + place(ti);
-        dst[0] = static_cast<uint16_t>(hi);
-        dst[kCol] = static_cast<uint16_t>(hi >> 16);
-        dst[kC * kCol] = static_cast<uint16_t>(lo);
-        dst[kC * kCol + kCol] = static_cast<uint16_t>(lo >> 16);
-      }
-    }
-    __syncthreads();
-
-    f32x4 dU[4] = {zero, zero, zero, zero};
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const Frag f = to_b(dS[2 * ks], dS[2 * ks + 1]);
-      if (live) store_packed(p.DS + (ci * KP + 32 * ks) * d.VP, poff, f, d.VP);
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-        dU[mt] = mma_split<NP>(s.k + (16 * mt + r) * kRow<KP> + 32 * ks + 8 * g, kC * kRow<KP>, f, dU[mt]);
-    }
-    f32x4 dO[4];
+    for (int i = 0; i < n; ++i) x[i] = at<h8>(base + i * kFrag, lane * 16);
+  };
+  auto KFp = [&](int64_t c) { return p.w.KF + (bg * d.nc + c) * (NP * NF * kFrag); };
+  auto KTp = [&](int64_t c) { return p.w.KT + (bg * d.nc + c) * (NP * NF * kFrag); };
+  auto QTp = [&](int64_t c) { return p.w.QT + (bg * d.nc + c) * (NP * NF * kFrag); };
+  auto load_p = [&](int64_t c) {
+    const uint16_t* x = p.w.PT + (bh * d.nc + c) * (12 * kFrag);
+    frags(ph, x, 6);
+    frags(pl, x + 6 * kFrag, 6);
+  };
+  auto load_t = [&](int64_t c) {
+    const uint16_t* x = p.w.TT + (bh * d.nc + c) * (12 * kFrag);
+    frags(th, x, 6);
+    frags(tl, x + 6 * kFrag, 6);
+  };
+  auto load_sc = [&](int64_t c) {
+    const float* x = p.w.hsc + (bh * d.nc + c) * (kHeadSc * kC);
+    sc[0] = x[H_BETA * kC + lane];
+    sc[1] = x[H_BK * kC + lane];
+    sc[2] = x[H_DK * kC + lane];
+    sc[3] = x[H_EQ * kC + lane];
+    el = x[H_E * kC + kC - 1];
+  };
+  auto load_v = [&](int64_t c) {
+    const int64_t left = d.T - c * kC;
+    const char* base = static_cast<const char*>(p.dy) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES);
+    const int64_t row = fresh(vrow);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int t = 16 * mt + 4 * g + e;
-        dO[mt][e] = ok && t < left ? IO<A>::ld(p.dy, ((b * d.T + t0 + t) * d.H + h) * d.V + col) * so : 0.0f;
-        dU[mt][e] *= exp2_fast(static_cast<float>(Gl - Gs[t])) * sc[SC_RK * kC + t];
+        v[mt][e] = 0u;
+        if (left >= kC || 16 * mt + 4 * g + e < left) v[mt][e] = at<Raw>(base + (16 * mt + e) * row, voff);
       }
+  };
+  if (AHEAD) {
+    frags(kf, KFp(d.nc - 1), NF);
+    load_p(d.nc - 1);
+    load_t(d.nc - 1);
+    frags(kt, KTp(d.nc - 1), NF);
+    frags(qt, QTp(d.nc - 1), NF);
+  }
+  load_sc(d.nc - 1);
+  load_v(d.nc - 1);
+  for (int64_t c = d.nc - 1; c >= 0; --c) {
+    const int64_t left = d.T - c * kC, ci = bh * d.nc + c;
+    const bool more = AHEAD && c > 0;
+    mscan::wave_lds_sync();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i][lane] = sc[i];
+    mscan::wave_lds_sync();
+    const float elc = el;
+    if (c > 0) load_sc(c - 1);
+    if (!AHEAD) {
+      frags(kf, KFp(c), NF);
+      load_p(c);
+    }
+    f32x4 dU[4] = {zero, zero, zero, zero}, pd[4] = {zero, zero, zero, zero}, dO[4];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const Frag f = to_b(dS[2 * ks], dS[2 * ks + 1]);
+      store_packed(p.DS + (ci * KP + 32 * ks) * d.VP, poff, f, d.VP);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(kf[mt * KS + ks], f.hi, dU[mt]);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(kf[mt * KS + ks], f.lo, dU[mt]);
+      if (NP == 2) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(at<h8>(KFp(c) + (NF + mt * KS + ks) * kFrag, lane * 16), f.hi, dU[mt]);
+      }
+    }
+    if (more) frags(kf, KFp(c - 1), NF);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dO[mt][e] = IO<A>::cvt(v[mt][e]) * soc;
+    if (c > 0) load_v(c - 1);
     const Frag o0 = to_b(dO[0], dO[1]), o1 = to_b(dO[2], dO[3]);   // 16-bit input: the low parts are zero
 #pragma unroll
+    for (int f = 0; f < 6; ++f) pd[kUm[f]] = mma(ph[f], (kUk[f] ? o1 : o0).hi, pd[kUm[f]]);
+#pragma unroll
+    for (int f = 0; f < 6; ++f) pd[kUm[f]] = mma(pl[f], (kUk[f] ? o1 : o0).hi, pd[kUm[f]]);
+    if (NP == 2) {
+#pragma unroll
+      for (int f = 0; f < 6; ++f) pd[kUm[f]] = mma(ph[f], (kUk[f] ? o1 : o0).lo, pd[kUm[f]]);
+    }
+    if (more) load_p(c - 1);
+    if (!AHEAD) {
+      load_t(c);
+      frags(kt, KTp(c), NF);
+      frags(qt, QTp(c), NF);
+    }
+#pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      f32x4 acc = zero;
+      const f32x4 dk = *reinterpret_cast<const f32x4*>(s[2] + 16 * mt + 4 * g), eq = *reinterpret_cast<const f32x4*>(s[3] + 16 * mt + 4 * g);
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        if (mt >= 2 && ks == 0) continue;
-        const uint16_t* a = s.PT + (16 * mt + r) * kCol + 32 * ks + 8 * g;
-        const Frag& o = ks ? o1 : o0;
-        const h8 ah = ld8(a);
-        acc = mma(ah, o.hi, acc);
-        acc = mma(ld8(a + kC * kCol), o.hi, acc);
-        if (NP == 2) acc = mma(ah, o.lo, acc);
+      for (int e = 0; e < 4; ++e) {
+        dU[mt][e] = fmaf(dU[mt][e], dk[e], pd[mt][e] * rps);
+        dO[mt][e] *= eq[e];
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dU[mt][e] = fmaf(acc[e], rps, dU[mt][e]);
     }
     const Frag u0 = to_b(dU[0], dU[1]), u1 = to_b(dU[2], dU[3]);
     f32x4 Y[4] = {zero, zero, zero, zero};
-    const uint16_t* T = p.w.TT + ci * (kTFrag * 512) + lane * 8;
 #pragma unroll
-    for (int f = 0; f < 6; ++f) {
-      const Frag& x = kTTk[f] ? u1 : u0;
-      const h8 th = ld8(T + f * 512), tl = ld8(T + (6 + f) * 512);
-      f32x4 a = Y[kTTm[f]];
-      a = mma(th, x.hi, a);
-      a = mma(th, x.lo, a);
-      Y[kTTm[f]] = mma(tl, x.hi, a);
+    for (int f = 0; f < 6; ++f) Y[kUm[f]] = mma(th[f], (kUk[f] ? u1 : u0).hi, Y[kUm[f]]);
+#pragma unroll
+    for (int f = 0; f < 6; ++f) Y[kUm[f]] = mma(th[f], (kUk[f] ? u1 : u0).lo, Y[kUm[f]]);
+#pragma unroll
+    for (int f = 0; f < 6; ++f) Y[kUm[f]] = mma(tl[f], (kUk[f] ? u1 : u0).hi, Y[kUm[f]]);
+    if (more) load_t(c - 1);
+    // e0, e1 and the state's part of dS from dO do not wait for Y
+    const Frag e0 = to_b(dO[0], dO[1]), e1 = to_b(dO[2], dO[3]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dS[mt][e] *= elc;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(qt[2 * mt], e0.hi, dS[mt]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(qt[2 * mt], e0.lo, dS[mt]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(qt[2 * mt + 1], e1.hi, dS[mt]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(qt[2 * mt + 1], e1.lo, dS[mt]);
+    if (NP == 2) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        dS[mt] = mma(at<h8>(QTp(c) + (NF + 2 * mt) * kFrag, lane * 16), e0.hi, dS[mt]);
+        dS[mt] = mma(at<h8>(QTp(c) + (NF + 2 * mt + 1) * kFrag, lane * 16), e1.hi, dS[mt]);
+      }
     }
+    if (more) frags(qt, QTp(c - 1), NF);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) Y[mt][e] *= 1.0f / kTScale;
-    if (live) {
-      store_packed(p.DU + ci * kC * d.VP, poff, to_b(Y[0], Y[1]), d.VP);
-      store_packed(p.DU + (ci * kC + 32) * d.VP, poff, to_b(Y[2], Y[3]), d.VP);
-    }
+    store_packed(p.DU + ci * kC * d.VP, poff, to_b(Y[0], Y[1]), d.VP);
+    store_packed(p.DU + (ci * kC + 32) * d.VP, poff, to_b(Y[2], Y[3]), d.VP);
+    char* out = static_cast<char*>(p.d_v) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES);
+    const int64_t yrow = fresh(vrow);
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int mt = 0; mt < 4; ++mt) {
+      const f32x4 be = *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * g), bk = *reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * g);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int t = 16 * mt + 4 * g + e;
-        const float be = sc[SC_BETA * kC + t], ev = sc[SC_E * kC + t];
-        const float dv = be * Y[mt][e];
-        if (ok && t < left) IO<A>::st(p.d_v, ((b * d.T + t0 + t) * d.H + h) * d.V + col, dv * rso);
-        Y[mt][e] = -(ev * sc[SC_RK * kC + t]) * dv;
-        dO[mt][e] *= ev * sc[SC_RQ * kC + t];
+        if (ok && (left >= kC || 16 * mt + 4 * g + e < left))
+          IO<A>::st(&at<char>(out + (16 * mt + e) * yrow, yoff), 0, be[e] * Y[mt][e] * rso);
+        Y[mt][e] *= -bk[e];
       }
-    const Frag y0 = to_b(Y[0], Y[1]), y1 = to_b(Y[2], Y[3]), e0 = to_b(dO[0], dO[1]), e1 = to_b(dO[2], dO[3]);
-    const float el = exp2_fast(static_cast<float>(Gl));
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dS[mt][e] *= el;
-      const uint16_t* a = s.kT + (16 * mt + r) * kCol + 8 * g;
-      const uint16_t* q = s.qT + (16 * mt + r) * kCol + 8 * g;
-      dS[mt] = mma_split<NP>(a, KP * kCol, y0, dS[mt]);
-      dS[mt] = mma_split<NP>(a + 32, KP * kCol, y1, dS[mt]);
-      dS[mt] = mma_split<NP>(q, KP * kCol, e0, dS[mt]);
-      dS[mt] = mma_split<NP>(q + 32, KP * kCol, e1, dS[mt]);
     }
+    const Frag y0 = to_b(Y[0], Y[1]), y1 = to_b(Y[2], Y[3]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(kt[2 * mt], y0.hi, dS[mt]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(kt[2 * mt], y0.lo, dS[mt]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(kt[2 * mt + 1], y1.hi, dS[mt]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(kt[2 * mt + 1], y1.lo, dS[mt]);
+    if (NP == 2) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        dS[mt] = mma(at<h8>(KTp(c) + (NF + 2 * mt) * kFrag, lane * 16), y0.hi, dS[mt]);
+        dS[mt] = mma(at<h8>(KTp(c) + (NF + 2 * mt + 1) * kFrag, lane * 16), y1.hi, dS[mt]);
+      }
+    }
+    if (more) frags(kt, KTp(c - 1), NF);
   }
 }
 
 // ------------------------------------------------------------------ the chunks' own gradients
 // One workgroup per (batch row, query / key head, chunk), over the value heads that share it.  First all products
-// with d_v contracted, in slabs of 32 columns: rows of dO, U and Y through LDS, S and dS' from global memory straight
-// into the fragments of the wave that owns their d_k rows.  Then the 64 x 64 gradients M1 and M2, and their products
-// with q and k.
+// with d_v contracted, in slabs of 32 columns: rows of dO, U and Y through LDS (the next slab's in flight), S and dS'
+// from global memory straight into the fragments of the wave that owns their d_k rows.  Then the 64 x 64 gradients M1
+// and M2 (ten lower tiles over the four waves), and their products with q and k.
 constexpr int kSlab = 32 + 8;
 
-template <Act A, int KP>
+template <Act A>
 struct ChunkLds {
   static constexpr int NP = A == Act::F32 ? 2 : 1;
   union {
     struct {
-      uint16_t dO[NP * kC * kSlab], U[2 * kC * kSlab], Y[2 * kC * kSlab];
-    };
+      uint16_t dO[NP][kC * kSlab], U[2][kC * kSlab], Y[2][kC * kSlab];
+    } slab[2];
     struct {
-      uint16_t k[NP * kC * kRow<KP>], q[NP * kC * kRow<KP>];
-    };
-    struct {
-      uint16_t kT[NP * KP * kCol], qT[NP * KP * kCol];
+      uint16_t M1[2][kC * kCol], M1T[2][kC * kCol], M2[2][kC * kCol], M2T[2][kC * kCol];
     };
   };
-  uint16_t M1[2 * kC * kCol], M1T[2 * kC * kCol], M2[2 * kC * kCol], M2T[2 * kC * kCol];
-  float rows[4][4][kC];   // per wave: row sums
-  float colE[kC], db[kC], red[8];
   double G[kC];
+  float beta[kC], e[kC], dec[kC], rk[kC], rq[kC], db[kC];
+  float rowE[4][kC], colE[4][kC];   // by column tile, by row tile
+  float rows[4][3][kC];             // by wave
+  float red[8];
 };
 
-__device__ __forceinline__ void unpack8(const uint32_t* p, h8& hi, h8& lo) {
-  const u32x4 a = *reinterpret_cast<const u32x4*>(p), b = *reinterpret_cast<const u32x4*>(p + 4);
+__device__ __forceinline__ void unpack8(u32x4 a, u32x4 b, h8& hi, h8& lo) {
   u32x4 h, l;
   h[0] = (a[0] & 0xffffu) | (a[1] << 16);
   h[1] = (a[2] & 0xffffu) | (a[3] << 16);
@@ -263,379 +303,423 @@ __device__ __forceinline__ void unpack8(const uint32_t* p, h8& hi, h8& lo) {
   lo = __builtin_bit_cast(h8, l);
 }
 
-__device__ __forceinline__ f32x4 mma3(h8 ah, h8 al, h8 bh, h8 bl, f32x4 c) {
-  c = mma(ah, bh, c);
-  c = mma(ah, bl, c);
-  return mma(al, bh, c);
-}
-
-template <Act A, int KP>
-__global__ void __launch_bounds__(256) gdelta_bwd_chunk_kernel(const BwdArgs p) {
-  constexpr int NP = A == Act::F32 ? 2 : 1, NT = KP / 64, KS = KP / 32;
-  __shared__ __attribute__((aligned(16))) ChunkLds<A, KP> s;
-  static_assert(sizeof(s) <= mscan::kLdsBytes, "LDS");
+template <Act A, int KP, bool SHARED>
+__global__ void __launch_bounds__(256, SHARED ? 1 : 2) gdelta_bwd_chunk_kernel(const BwdArgs p) {
+  constexpr int NP = A == Act::F32 ? 2 : 1, NT = KP / 64, KS = KP / 32, NF = KP / 8;
+  __shared__ __attribute__((aligned(16))) ChunkLds<A> s;
+  static_assert(sizeof(s) <= mscan::kLdsBytes / 2, "two workgroups a CU");
   const Dims& d = p.d;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, r = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
   const int64_t c = blockIdx.x % d.nc, bg = blockIdx.x / d.nc, hk = bg % d.G, b = bg / d.G;
-  const int64_t t0 = c * kC, left = d.T - t0;
-  const int share = static_cast<int>(d.H / d.G);
+  const int64_t t0 = c * kC, left = d.T - t0, gi = bg * d.nc + c;
+  const int share = SHARED ? static_cast<int>(d.H / d.G) : 1;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t qk = ((b * d.T + t0) * d.G + hk) * d.K;
-  const int n0 = wv * (KP / 4);   // this wave's d_k columns: n0 + 16 n + r
+  const int n0 = wv * NT;   // this wave's d_k tiles: n0 .. n0 + NT - 1
+  const float* gsc = p.w.gsc + gi * (kGroupSc * kC);
+  const uint16_t* KF = p.w.KF + gi * (NP * NF * kFrag);
+  const uint16_t* QF = p.w.QF + gi * (NP * NF * kFrag);
+  const uint16_t* KT = p.w.KT + gi * (NP * NF * kFrag);
+  const uint16_t* QT = p.w.QT + gi * (NP * NF * kFrag);
   f32x4 totQ[4][NT], totK[4][NT];
-#pragma unroll
-  for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) totQ[mt][n] = totK[mt][n] = zero;
+  h8 kt[NP][NT][2], qt[NP][NT][2];   // elements 0 .. 3: token rows 4 g + e of tile 2 ks, 4 .. 7: of tile 2 ks + 1
 
   for (int hi_ = 0; hi_ < share; ++hi_) {
     const int64_t h = hk * share + hi_, bh = b * d.H + h, ci = bh * d.nc + c;
-    const float* sc = p.w.sc + ci * (kSc * kC);
-    const float so = p.so[bh], sv = p.w.sv[bh], rso = 1.0f / so, rsv = 1.0f / sv;
-    f32x4 aP[4], aA[4], aQ[4][NT], aKq[4][NT], aKs[4][NT];
+    const float so = p.so[bh], rso = 1.0f / so, rsv = 1.0f / p.w.sv[bh];
+    f32x4 aP[3], aA[3], aQ[4][NT], aKq[4][NT], aKs[4][NT];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      aP[mt] = aA[mt] = zero;
+    for (int i = 0; i < 3; ++i) aP[i] = aA[i] = zero;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int n = 0; n < NT; ++n) aQ[mt][n] = aKq[mt][n] = aKs[mt][n] = zero;
-    }
     float dot = 0.0f;   // <dS', S>
+    // a thread's part of a slab: 8 columns of one token
+    const int t = tid >> 2, cc = (tid & 3) * 8;
+    u32x4 ru[2], ry[2], ro[NP], rs[NT][2], rd[NT][2];
+    const uint32_t uoff = (t * d.VP + cc) * 4, soff = (r * d.VP + 8 * g) * 4;
+    const char* dyb = static_cast<const char*>(p.dy) + ((b * d.T + t0) * d.H + h) * (d.V * (NP * 2));
+    const uint32_t dyoff = (static_cast<uint32_t>(t) * static_cast<uint32_t>(d.H * d.V) + cc) * (NP * 2);
+    auto load_rows = [&](int v0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ru[i] = at<u32x4>(p.w.U + ci * kC * d.VP + v0 + 4 * i, uoff);
+        ry[i] = at<u32x4>(p.DU + ci * kC * d.VP + v0 + 4 * i, uoff);
+      }
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        ro[i] = u32x4{0u, 0u, 0u, 0u};
+        if (t < left && v0 + cc < d.V) ro[i] = at<u32x4>(dyb + v0 * (NP * 2) + 16 * i, dyoff);
+      }
+    };
+    auto load_states = [&](int v0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          rs[n][i] = at<u32x4>(p.w.S + (ci * KP + 16 * (n0 + n)) * d.VP + v0 + 4 * i, soff);
+          rd[n][i] = at<u32x4>(p.DS + (ci * KP + 16 * (n0 + n)) * d.VP + v0 + 4 * i, soff);
+        }
+    };
+    load_rows(0);
+    load_states(0);
+    if (tid < kC) {
+      const float* sc = p.w.hsc + ci * (kHeadSc * kC);
+      const double G = p.w.G[ci * kC + tid], Gl = p.w.G[ci * kC + kC - 1];
+      s.G[tid] = G;
+      s.beta[tid] = sc[H_BETA * kC + tid];
+      s.e[tid] = sc[H_E * kC + tid];
+      s.dec[tid] = exp2_fast(static_cast<float>(Gl - G));
+      s.rk[tid] = gsc[G_RK * kC + tid];
+      s.rq[tid] = gsc[G_RQ * kC + tid];
+    }
     for (int v0 = 0; v0 < d.VP; v0 += 32) {
-      __syncthreads();
+      auto& sl = s.slab[(v0 >> 5) & 1];
       {
-        const int t = tid >> 2, cc = (tid & 3) * 8;
-        float x[8];
-        load8<A>(p.dy, ((b * d.T + t0 + t) * d.H + h) * d.V + v0 + cc, t < left && v0 + cc < d.V, x);
+        h8 ph, pl;
+        unpack8(ru[0], ru[1], ph, pl);
+        *reinterpret_cast<h8*>(sl.U[0] + t * kSlab + cc) = ph;
+        *reinterpret_cast<h8*>(sl.U[1] + t * kSlab + cc) = pl;
+        unpack8(ry[0], ry[1], ph, pl);
+        *reinterpret_cast<h8*>(sl.Y[0] + t * kSlab + cc) = ph;
+        *reinterpret_cast<h8*>(sl.Y[1] + t * kSlab + cc) = pl;
         u32x4 hi, lo;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
+          float x, y;
+          if constexpr (NP == 2) {
+            x = __builtin_bit_cast(float, static_cast<uint32_t>(ro[e >> 1][(e & 1) * 2]));
+            y = __builtin_bit_cast(float, static_cast<uint32_t>(ro[e >> 1][(e & 1) * 2 + 1]));
+          } else {
+            x = IO<A>::cvt(ro[0][e] & 0xffffu);
+            y = IO<A>::cvt(ro[0][e] >> 16);
+          }
           uint32_t a, bb;
-          split2(x[2 * e] * so, x[2 * e + 1] * so, a, bb);
+          split2(x * so, y * so, a, bb);
           hi[e] = a;
           lo[e] = bb;
         }
-        *reinterpret_cast<u32x4*>(s.dO + t * kSlab + cc) = hi;
-        if (NP == 2) *reinterpret_cast<u32x4*>(s.dO + kC * kSlab + t * kSlab + cc) = lo;
-        h8 ph, pl;
-        unpack8(p.w.U + (ci * kC + t) * d.VP + v0 + cc, ph, pl);
-        *reinterpret_cast<h8*>(s.U + t * kSlab + cc) = ph;
-        *reinterpret_cast<h8*>(s.U + kC * kSlab + t * kSlab + cc) = pl;
-        unpack8(p.DU + (ci * kC + t) * d.VP + v0 + cc, ph, pl);
-        *reinterpret_cast<h8*>(s.Y + t * kSlab + cc) = ph;
-        *reinterpret_cast<h8*>(s.Y + kC * kSlab + t * kSlab + cc) = pl;
+        *reinterpret_cast<u32x4*>(sl.dO[0] + t * kSlab + cc) = hi;
+        if (NP == 2) *reinterpret_cast<u32x4*>(sl.dO[NP - 1] + t * kSlab + cc) = lo;
       }
-      __syncthreads();
-      h8 sh[NT], sl[NT], gh[NT], gl[NT];
+      h8 sh[NT], slo[NT], gh[NT], gl[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int64_t at = (ci * KP + n0 + 16 * n + r) * d.VP + v0 + 8 * g;
-        unpack8(p.w.S + at, sh[n], sl[n]);
-        unpack8(p.DS + at, gh[n], gl[n]);
+        unpack8(rs[n][0], rs[n][1], sh[n], slo[n]);
+        unpack8(rd[n][0], rd[n][1], gh[n], gl[n]);
+      }
+      if (v0 + 32 < d.VP) {
+        load_rows(v0 + 32);
+        load_states(v0 + 32);
+      }
+      mscan::lds_barrier();
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          dot = fmaf(static_cast<float>(sh[n][e]) + static_cast<float>(sl[n][e]),
+          dot = fmaf(static_cast<float>(sh[n][e]) + static_cast<float>(slo[n][e]),
                      static_cast<float>(gh[n][e]) + static_cast<float>(gl[n][e]), dot);
-      }
-      const int bt = (16 * wv + r) * kSlab + 8 * g;
-      const h8 ubh = ld8(s.U + bt), ubl = ld8(s.U + kC * kSlab + bt);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
-        const int at = (16 * mt + r) * kSlab + 8 * g;
-        const h8 oh = ld8(s.dO + at), uh = ld8(s.U + at), ul = ld8(s.U + kC * kSlab + at);
-        const h8 yh = ld8(s.Y + at), yl = ld8(s.Y + kC * kSlab + at);
-        h8 ol = {};
-        if (NP == 2) ol = ld8(s.dO + kC * kSlab + at);
-        if (mt >= wv) {
-          aP[mt] = mma(oh, ubh, aP[mt]);
-          aP[mt] = mma(oh, ubl, aP[mt]);
-          if (NP == 2) aP[mt] = mma(ol, ubh, aP[mt]);
-          aA[mt] = mma3(yh, yl, ubh, ubl, aA[mt]);
-        }
+        const int a = (16 * mt + r) * kSlab + 8 * g;
+        const h8 oh = ld8(sl.dO[0] + a), uh = ld8(sl.U[0] + a), ul = ld8(sl.U[1] + a);
+        const h8 yh = ld8(sl.Y[0] + a), yl = ld8(sl.Y[1] + a);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           aQ[mt][n] = mma(oh, sh[n], aQ[mt][n]);
-          aQ[mt][n] = mma(oh, sl[n], aQ[mt][n]);
-          if (NP == 2) aQ[mt][n] = mma(ol, sh[n], aQ[mt][n]);
-          aKq[mt][n] = mma3(yh, yl, sh[n], sl[n], aKq[mt][n]);
-          aKs[mt][n] = mma3(uh, ul, gh[n], gl[n], aKs[mt][n]);
+          aKq[mt][n] = mma(yh, sh[n], aKq[mt][n]);
+          aKs[mt][n] = mma(uh, gh[n], aKs[mt][n]);
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          aQ[mt][n] = mma(oh, slo[n], aQ[mt][n]);
+          aKq[mt][n] = mma(yh, slo[n], aKq[mt][n]);
+          aKs[mt][n] = mma(uh, gl[n], aKs[mt][n]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          aKq[mt][n] = mma(yl, sh[n], aKq[mt][n]);
+          aKs[mt][n] = mma(ul, gh[n], aKs[mt][n]);
+          if (NP == 2) aQ[mt][n] = mma(ld8(sl.dO[NP - 1] + a), sh[n], aQ[mt][n]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {   // lower tiles wv, wv + 4, wv + 8
+        const int tl = wv + 4 * i;
+        if (tl >= 10) break;
+        const int mt = tl < 1 ? 0 : tl < 3 ? 1 : tl < 6 ? 2 : 3, nt = tl - mt * (mt + 1) / 2;
+        const int a = (16 * mt + r) * kSlab + 8 * g, bb = (16 * nt + r) * kSlab + 8 * g;
+        const h8 oh = ld8(sl.dO[0] + a), yh = ld8(sl.Y[0] + a), yl = ld8(sl.Y[1] + a);
+        const h8 uh = ld8(sl.U[0] + bb), ul = ld8(sl.U[1] + bb);
+        aP[i] = mma(oh, uh, aP[i]);
+        aA[i] = mma(yh, uh, aA[i]);
+        aP[i] = mma(oh, ul, aP[i]);
+        aA[i] = mma(yh, ul, aA[i]);
+        if (NP == 2) aP[i] = mma(ld8(sl.dO[NP - 1] + a), uh, aP[i]);
+        aA[i] = mma(yl, uh, aA[i]);
       }
     }
-    __syncthreads();
-    if (tid < kC) s.G[tid] = p.w.G[ci * kC + tid];
-    stage_qk<A, KP, 256>(p.k, p.q, qk, d.G * d.K, d.K, left, sc, s.k, s.q, nullptr, nullptr, tid);
-    __syncthreads();
-    // this wave's columns j of the 64 x 64 gradients
-    const int j = 16 * wv + r;
-    const float rkj = sc[SC_RK * kC + j];
-    f32x4 m1[4], m2[4];
-    float ce = 0.0f, big = 0.0f;
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      m1[mt] = m2[mt] = zero;
-      f32x4 kq = zero, kk = zero;
-      if (mt >= wv) {
+    for (int pl = 0; pl < NP; ++pl)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const int at = (16 * mt + r) * kRow<KP> + 32 * ks + 8 * g, bt = j * kRow<KP> + 32 * ks + 8 * g;
-          const h8 bk = ld8(s.k + bt), aq = ld8(s.q + at), ak = ld8(s.k + at);
-          kq = mma(aq, bk, kq);
-          kk = mma(ak, bk, kk);
-          if (NP == 2) {
-            const h8 bl = ld8(s.k + kC * kRow<KP> + bt);
-            kq = mma(aq, bl, kq);
-            kk = mma(ak, bl, kk);
-            kq = mma(ld8(s.q + kC * kRow<KP> + at), bk, kq);
-            kk = mma(ld8(s.k + kC * kRow<KP> + at), bk, kk);
-          }
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          kt[pl][n][ks] = at<h8>(KT + (pl * NF + 2 * (n0 + n) + ks) * kFrag, lane * 16);
+          qt[pl][n][ks] = at<h8>(QT + (pl * NF + 2 * (n0 + n) + ks) * kFrag, lane * 16);
         }
-      }
+    // this wave's tiles of the 64 x 64 gradients, and of E
+    f32x4 m1[3], m2[3];
+    float big = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      m1[i] = m2[i] = zero;
+      const int tl = wv + 4 * i;
+      if (tl >= 10) break;
+      const int mt = tl < 1 ? 0 : tl < 3 ? 1 : tl < 6 ? 2 : 3, nt = tl - mt * (mt + 1) / 2, j = 16 * nt + r;
+      const f32x4 kq = frag_mm<NP, KS, NF>(QF + mt * KS * kFrag, KF + nt * KS * kFrag, lane, zero);
+      const f32x4 kk = frag_mm<NP, KS, NF>(KF + mt * KS * kFrag, KF + nt * KS * kFrag, lane, zero);
+      const float rkj = s.rk[j];
+      const double Gj = s.G[j];
+      float ce = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = 16 * mt + 4 * g + e;
-        const float rq = sc[SC_RQ * kC + i], rk = sc[SC_RK * kC + i], be = sc[SC_BETA * kC + i];
-        const float D = j <= i ? exp2_fast(static_cast<float>(s.G[i] - s.G[j])) : 0.0f;
-        const float dP = aP[mt][e] * rso * rsv, yu = aA[mt][e] * rso * rsv;
+        const int ti = 16 * mt + 4 * g + e;
+        const float rq = s.rq[ti], rk = s.rk[ti], be = s.beta[ti];
+        const float D = j <= ti ? exp2_fast(static_cast<float>(s.G[ti] - Gj)) : 0.0f;
+        const float dP = aP[i][e] * rso * rsv, yu = aA[i][e] * rso * rsv;
         float E = 0.0f;
-        m1[mt][e] = j <= i ? dP * D : 0.0f;
-        if (j < i) {
-          m2[mt][e] = -yu * be * D;
-          E = m1[mt][e] * (rq * rkj * kq[e]) + m2[mt][e] * (rk * rkj * kk[e]);
+        m1[i][e] = j <= ti ? dP * D : 0.0f;
+        if (j < ti) {
+          m2[i][e] = -yu * be * D;
+          E = m1[i][e] * (rq * rkj * kq[e]) + m2[i][e] * (rk * rkj * kk[e]);
         }
-        if (i == j) s.db[i] = yu * (1.0f - be);
+        if (ti == j) s.db[ti] = yu * (1.0f - be);
         ce += E;
         const float re = sum16(E);
-        if (r == 0) s.rows[wv][0][i] = re;
-        const float a = fmaxf(fabsf(m1[mt][e]), fabsf(m2[mt][e])) * fmaxf(rkj, fmaxf(fabsf(rq), rk));
-        big = max_finite(big, a);
+        if (r == 0) s.rowE[nt][ti] = re;
+        big = max_finite(big, fmaxf(fabsf(m1[i][e]), fabsf(m2[i][e])) * fmaxf(rkj, fmaxf(fabsf(rq), rk)));
       }
+      ce += __shfl_xor(ce, 16, 64);
+      ce += __shfl_xor(ce, 32, 64);
+      if (g == 0) s.colE[mt][j] = ce;
     }
-    ce += __shfl_xor(ce, 16, 64);
-    ce += __shfl_xor(ce, 32, 64);
-    if (g == 0) s.colE[j] = ce;
     big = wave_max(big);
     dot = wave_sum(dot);
     if (lane == 0) {
       s.red[wv] = big;
       s.red[4 + wv] = dot;
     }
-    __syncthreads();   // k, q read; s.red written
-    stage_qk<A, KP, 256>(p.k, p.q, qk, d.G * d.K, d.K, left, sc, nullptr, nullptr, s.kT, s.qT, tid);
+    __syncthreads();   // the slabs are read, s.red written
     const float sm = pow2_below(fmaxf(fmaxf(s.red[0], s.red[1]), fmaxf(s.red[2], s.red[3])), 13), rsm = 1.0f / sm;
-    dot = s.red[4] + s.red[5] + s.red[6] + s.red[7];
+    dot = (s.red[4] + s.red[5]) + (s.red[6] + s.red[7]);
+    {   // zeros in the tiles past the diagonal that a 32-wide step reads: (0, 1), (2, 3), and (1, 0), (3, 2) of the transposes
+      const int pl = tid >> 7, tile = (tid >> 6) & 1, row = (tid >> 2) & 15, q = tid & 3;
+      const int up = (32 * tile + row) * kCol + 32 * tile + 8 * q + 4, dn = (32 * tile + 16 + row) * kCol + 32 * tile + 8 * q;
+      *reinterpret_cast<u32x2*>(s.M1[pl] + up) = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(s.M2[pl] + up) = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(s.M1T[pl] + dn) = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(s.M2T[pl] + dn) = u32x2{0u, 0u};
+    }
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      const int i0 = 16 * mt + 4 * g;
+    for (int i = 0; i < 3; ++i) {
+      const int tl = wv + 4 * i;
+      if (tl >= 10) break;
+      const int mt = tl < 1 ? 0 : tl < 3 ? 1 : tl < 6 ? 2 : 3, nt = tl - mt * (mt + 1) / 2, j = 16 * nt + r, i0 = 16 * mt + 4 * g;
+      const float rkj = s.rk[j];
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
-        const f32x4 m = which ? m2[mt] : m1[mt];
-        uint16_t* a = (which ? s.M2 : s.M1) + i0 * kCol + place(j);
-        uint16_t* at = (which ? s.M2T : s.M1T) + j * kCol + place(i0);
-        uint32_t h[2], l[2], th[2], tl[2];
+        const f32x4 m = which ? m2[i] : m1[i];
+        const float* ri = (which ? s.rk : s.rq) + i0;
+        const int a = i0 * kCol + place(j), at_ = j * kCol + place(i0);
+        uint16_t* hp = which ? s.M2[0] : s.M1[0];
+        uint16_t* lp = which ? s.M2[1] : s.M1[1];
+        uint32_t th[2], tlo[2];
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
           const float x = m[2 * o] * sm, y = m[2 * o + 1] * sm;
-          const float* ri = sc + (which ? SC_RK : SC_RQ) * kC + i0 + 2 * o;
-          split2(x * rkj, y * rkj, h[o], l[o]);
-          split2(x * ri[0], y * ri[1], th[o], tl[o]);
-          a[(2 * o) * kCol] = static_cast<uint16_t>(h[o]);
-          a[(2 * o + 1) * kCol] = static_cast<uint16_t>(h[o] >> 16);
-          a[kC * kCol + (2 * o) * kCol] = static_cast<uint16_t>(l[o]);
-          a[kC * kCol + (2 * o + 1) * kCol] = static_cast<uint16_t>(l[o] >> 16);
+          uint32_t hh, ll;
+          split2(x * rkj, y * rkj, hh, ll);
+          split2(x * ri[2 * o], y * ri[2 * o + 1], th[o], tlo[o]);
+          hp[a + (2 * o) * kCol] = static_cast<uint16_t>(hh);
+          hp[a + (2 * o + 1) * kCol] = static_cast<uint16_t>(hh >> 16);
+          lp[a + (2 * o) * kCol] = static_cast<uint16_t>(ll);
+          lp[a + (2 * o + 1) * kCol] = static_cast<uint16_t>(ll >> 16);
         }
-        *reinterpret_cast<u32x2*>(at) = u32x2{th[0], th[1]};
-        *reinterpret_cast<u32x2*>(at + kC * kCol) = u32x2{tl[0], tl[1]};
+        *reinterpret_cast<u32x2*>((which ? s.M2T[0] : s.M1T[0]) + at_) = u32x2{th[0], th[1]};
+        *reinterpret_cast<u32x2*>((which ? s.M2T[1] : s.M1T[1]) + at_) = u32x2{tlo[0], tlo[1]};
       }
     }
-    __syncthreads();
     // the parts through the state, in true units, and their products with q and k for the decay's gradient
-    const double Gl = s.G[kC - 1];
+    auto elem = [&](const h8 (&x)[NP][NT][2], int n, int mt, int e) {
+      float v = static_cast<float>(x[0][n][mt >> 1][(mt & 1) * 4 + e]);
+      if (NP == 2) v += static_cast<float>(x[NP - 1][n][mt >> 1][(mt & 1) * 4 + e]);
+      return v;
+    };
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      const int i0 = 16 * mt + 4 * g;
-      float wq[4] = {}, wkq[4] = {}, wks[4] = {};
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int at = (n0 + 16 * n + r) * kCol + place(i0);
-        f32x4 kv, qv;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          kv[e] = static_cast<float>(reinterpret_cast<const h4*>(s.kT + at)[0][e]);
-          qv[e] = static_cast<float>(reinterpret_cast<const h4*>(s.qT + at)[0][e]);
-          if (NP == 2) {
-            kv[e] += static_cast<float>(reinterpret_cast<const h4*>(s.kT + KP * kCol + at)[0][e]);
-            qv[e] += static_cast<float>(reinterpret_cast<const h4*>(s.qT + KP * kCol + at)[0][e]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = i0 + e;
-          const float ev = sc[SC_E * kC + i], be = sc[SC_BETA * kC + i];
-          aQ[mt][n][e] *= ev * rso * rsv;
-          aKq[mt][n][e] *= -(ev * be) * rso * rsv;
-          aKs[mt][n][e] *= exp2_fast(static_cast<float>(Gl - s.G[i])) * rso * rsv;
-          wq[e] = fmaf(aQ[mt][n][e], qv[e], wq[e]);
-          wkq[e] = fmaf(aKq[mt][n][e], kv[e], wkq[e]);
-          wks[e] = fmaf(aKs[mt][n][e], kv[e], wks[e]);
-        }
-      }
+    for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float x = sum16(wq[e]), y = sum16(wkq[e]), z = sum16(wks[e]);
+        const int ti = 16 * mt + 4 * g + e;
+        const float ev = s.e[ti], be = s.beta[ti], de = s.dec[ti];
+        float wq = 0.0f, wkq = 0.0f, wks = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          aQ[mt][n][e] *= ev * rso * rsv;
+          aKq[mt][n][e] *= -(ev * be) * rso * rsv;
+          aKs[mt][n][e] *= de * rso * rsv;
+          const float kv = elem(kt, n, mt, e);
+          wq = fmaf(aQ[mt][n][e], elem(qt, n, mt, e), wq);
+          wkq = fmaf(aKq[mt][n][e], kv, wkq);
+          wks = fmaf(aKs[mt][n][e], kv, wks);
+        }
+        wq = sum16(wq);
+        wkq = sum16(wkq);
+        wks = sum16(wks);
         if (r == 0) {
-          const int i = i0 + e;
-          s.rows[wv][1][i] = x * sc[SC_RQ * kC + i];
-          s.rows[wv][2][i] = y * sc[SC_RK * kC + i];
-          s.rows[wv][3][i] = z * sc[SC_RK * kC + i];
+          s.rows[wv][0][ti] = wq * s.rq[ti];
+          s.rows[wv][1][ti] = wkq * s.rk[ti];
+          s.rows[wv][2][ti] = wks * s.rk[ti];
         }
       }
-    }
+    mscan::lds_barrier();
     // the parts inside the chunk
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
+      f32x4 q[NT], k[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        f32x4 q = aQ[mt][n], k = aKq[mt][n] + aKs[mt][n];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          q[e] *= sm;
-          k[e] *= sm;
+          q[n][e] = aQ[mt][n][e] * sm;
+          k[n][e] = (aKq[mt][n][e] + aKs[mt][n][e]) * sm;
         }
-        const int nr = (n0 + 16 * n + r) * kCol + 8 * g, ar = (16 * mt + r) * kCol + 8 * g;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const h8 kh = ld8(s.kT + nr + 32 * ks), qh = ld8(s.qT + nr + 32 * ks);
-          h8 kl = {}, ql = {};
-          if (NP == 2) {
-            kl = ld8(s.kT + KP * kCol + nr + 32 * ks);
-            ql = ld8(s.qT + KP * kCol + nr + 32 * ks);
-          }
-          const int a = ar + 32 * ks;
-          if (ks == 0 || mt >= 2) {   // rows i, columns j <= i
-            const h8 x = ld8(s.M1 + a), y = ld8(s.M2 + a);
-            q = mma(x, kh, q);
-            q = mma(ld8(s.M1 + kC * kCol + a), kh, q);
-            k = mma(y, kh, k);
-            k = mma(ld8(s.M2 + kC * kCol + a), kh, k);
+      for (int ks = 0; ks < 2; ++ks) {
+        const int a = (16 * mt + r) * kCol + 8 * g + 32 * ks;
+        if (ks == 0 || mt >= 2) {   // rows i, columns j <= i
+          const h8 xh = ld8(s.M1[0] + a), xl = ld8(s.M1[1] + a), yh = ld8(s.M2[0] + a), yl = ld8(s.M2[1] + a);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            q[n] = mma(xh, kt[0][n][ks], q[n]);
+            k[n] = mma(yh, kt[0][n][ks], k[n]);
+            q[n] = mma(xl, kt[0][n][ks], q[n]);
+            k[n] = mma(yl, kt[0][n][ks], k[n]);
             if (NP == 2) {
-              q = mma(x, kl, q);
-              k = mma(y, kl, k);
-            }
-          }
-          if (ks == 1 || mt < 2) {    // rows j, columns i >= j
-            const h8 x = ld8(s.M1T + a), y = ld8(s.M2T + a);
-            k = mma(x, qh, k);
-            k = mma(ld8(s.M1T + kC * kCol + a), qh, k);
-            k = mma(y, kh, k);
-            k = mma(ld8(s.M2T + kC * kCol + a), kh, k);
-            if (NP == 2) {
-              k = mma(x, ql, k);
-              k = mma(y, kl, k);
+              q[n] = mma(xh, kt[NP - 1][n][ks], q[n]);
+              k[n] = mma(yh, kt[NP - 1][n][ks], k[n]);
             }
           }
         }
+        if (ks == 1 || mt < 2) {    // rows j, columns i >= j
+          const h8 xh = ld8(s.M1T[0] + a), xl = ld8(s.M1T[1] + a), yh = ld8(s.M2T[0] + a), yl = ld8(s.M2T[1] + a);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          totQ[mt][n][e] += q[e] * rsm;
-          totK[mt][n][e] += k[e] * rsm;
+          for (int n = 0; n < NT; ++n) {
+            k[n] = mma(xh, qt[0][n][ks], k[n]);
+            k[n] = mma(xl, qt[0][n][ks], k[n]);
+            k[n] = mma(yh, kt[0][n][ks], k[n]);
+            k[n] = mma(yl, kt[0][n][ks], k[n]);
+            if (NP == 2) {
+              k[n] = mma(xh, qt[NP - 1][n][ks], k[n]);
+              k[n] = mma(yh, kt[NP - 1][n][ks], k[n]);
+            }
+          }
         }
       }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          totQ[mt][n][e] = (SHARED && hi_ ? totQ[mt][n][e] : 0.0f) + q[n][e] * rsm;
+          totK[mt][n][e] = (SHARED && hi_ ? totK[mt][n][e] : 0.0f) + k[n][e] * rsm;
+        }
     }
-    __syncthreads();
     if (tid < kC) {   // dg and what comes of it
-      const int t = tid;
       float x = 0.0f, z = 0.0f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        x += s.rows[w][1][t] + s.rows[w][2][t];
-        z += s.rows[w][3][t];
+        x += s.rows[w][0][tid] + s.rows[w][1][tid];
+        z += s.rows[w][2][tid];
       }
-      float E = 0.0f;
+      float E = 0.0f, C = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        if (w <= (t >> 4)) E += s.rows[w][0][t];
-      float dG = (E - s.colE[t]) + (x - z);
+      for (int w = 0; w < 4; ++w) {
+        if (w <= (tid >> 4)) E += s.rowE[w][tid];
+        if (w >= (tid >> 4)) C += s.colE[w][tid];
+      }
+      float dG = (E - C) + (x - z);
       // suffix sum over the chunk's tokens
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const float up = __shfl_down(dG, o, 64);
-        if (t + o < 64) dG += up;
+        if (tid + o < 64) dG += up;
       }
-      const float through = wave_sum(z) + exp2_fast(static_cast<float>(Gl)) * (dot * rso * rsv);
+      const float through = wave_sum(z) + s.e[kC - 1] * (dot * rso * rsv);
       float dg = dG + through;
-      if (!p.has_h0 && c == 0 && t == 0) dg = 0.0f;   // the first token's decay meets no state: exactly zero
+      if (!p.has_h0 && c == 0 && tid == 0) dg = 0.0f;   // the first token's decay meets no state: exactly zero
       float pa = 0.0f, pb = 0.0f;
-      if (t < left) {
-        const int64_t i = (b * d.T + t0 + t) * d.H + h;
+      if (tid < left) {
+        const int64_t i = (b * d.T + t0 + tid) * d.H + h;
         const float rate = exp2_fast(p.a_log[h] * kLog2e), z2 = p.a_raw[i] + p.dt_bias[h];
         const float da = -rate * mscan::sigmoid(z2) * dg;
         p.d_a_raw[i] = da;
-        p.d_b_raw[i] = s.db[t];
+        p.d_b_raw[i] = s.db[tid];
         pa = -rate * mscan::softplus(z2) * dg;
         pb = da;
       }
       pa = wave_sum(pa);
       pb = wave_sum(pb);
-      if (t == 0) {
+      if (tid == 0) {
         p.part[ci * 2] = pa;
         p.part[ci * 2 + 1] = pb;
       }
     }
+    __syncthreads();   // M, rows and the scalars are read
   }
-  // unit length's adjoint: r (d - n (n . d)); rows of q and k in kT, qT still
-  const int64_t ci = (b * d.H + hk * share) * d.nc + c;
-  const float* sc = p.w.sc + ci * (kSc * kC);
-  __syncthreads();
+  // unit length's adjoint: r (d - n (n . d))
 #pragma unroll
-  for (int mt = 0; mt < 4; ++mt) {
-    const int i0 = 16 * mt + 4 * g;
-    float wq[4] = {}, wk[4] = {};
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int at = (n0 + 16 * n + r) * kCol + place(i0);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float kv = static_cast<float>(reinterpret_cast<const h4*>(s.kT + at)[0][e]);
-        float qv = static_cast<float>(reinterpret_cast<const h4*>(s.qT + at)[0][e]);
-        if (NP == 2) {
-          kv += static_cast<float>(reinterpret_cast<const h4*>(s.kT + KP * kCol + at)[0][e]);
-          qv += static_cast<float>(reinterpret_cast<const h4*>(s.qT + KP * kCol + at)[0][e]);
-        }
-        wq[e] = fmaf(totQ[mt][n][e], qv, wq[e]);
-        wk[e] = fmaf(totK[mt][n][e], kv, wk[e]);
-      }
-    }
+  for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float x = sum16(wq[e]), y = sum16(wk[e]);
-      if (r == 0) {
-        s.rows[wv][0][i0 + e] = x;
-        s.rows[wv][1][i0 + e] = y;
-      }
-    }
-  }
-  __syncthreads();
-  const float rscale = 1.0f / d.scale;
-#pragma unroll
-  for (int mt = 0; mt < 4; ++mt) {
-    const int i0 = 16 * mt + 4 * g;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + e;
-      if (i >= left) continue;
-      const float pq = sc[SC_PQ * kC + i], rq = sc[SC_RQ * kC + i], pk = sc[SC_PK * kC + i], rk = sc[SC_RK * kC + i];
-      const float un = rq * rscale;
-      const float wq = (s.rows[0][0][i] + s.rows[1][0][i] + s.rows[2][0][i] + s.rows[3][0][i]) * un * un;
-      const float wk = (s.rows[0][1][i] + s.rows[1][1][i] + s.rows[2][1][i] + s.rows[3][1][i]) * rk * rk;
+      float wq = 0.0f, wk = 0.0f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int col = n0 + 16 * n + r, at = col * kCol + place(i0);
-        if (col >= d.K) continue;
-        float kv = static_cast<float>(reinterpret_cast<const h4*>(s.kT + at)[0][e]);
-        float qv = static_cast<float>(reinterpret_cast<const h4*>(s.qT + at)[0][e]);
+        float kv = static_cast<float>(kt[0][n][mt >> 1][(mt & 1) * 4 + e]), qv = static_cast<float>(qt[0][n][mt >> 1][(mt & 1) * 4 + e]);
         if (NP == 2) {
-          kv += static_cast<float>(reinterpret_cast<const h4*>(s.kT + KP * kCol + at)[0][e]);
-          qv += static_cast<float>(reinterpret_cast<const h4*>(s.qT + KP * kCol + at)[0][e]);
+          kv += static_cast<float>(kt[NP - 1][n][mt >> 1][(mt & 1) * 4 + e]);
+          qv += static_cast<float>(qt[NP - 1][n][mt >> 1][(mt & 1) * 4 + e]);
+        }
+        wq = fmaf(totQ[mt][n][e], qv, wq);
+        wk = fmaf(totK[mt][n][e], kv, wk);
+      }
+      wq = sum16(wq);
+      wk = sum16(wk);
+      if (r == 0) {
+        s.rows[wv][0][16 * mt + 4 * g + e] = wq;
+        s.rows[wv][1][16 * mt + 4 * g + e] = wk;
+      }
+    }
+  __syncthreads();
+  const float rscale = 1.0f / d.scale;
+  const int64_t qk = ((b * d.T + t0) * d.G + hk) * d.K;
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * mt + 4 * g + e;
+      if (i >= left) continue;
+      const float pq = gsc[G_PQ * kC + i], rq = s.rq[i], pk = gsc[G_PK * kC + i], rk = s.rk[i];
+      const float un = rq * rscale;
+      const float wq = ((s.rows[0][0][i] + s.rows[1][0][i]) + (s.rows[2][0][i] + s.rows[3][0][i])) * un * un;
+      const float wk = ((s.rows[0][1][i] + s.rows[1][1][i]) + (s.rows[2][1][i] + s.rows[3][1][i])) * rk * rk;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int col = 16 * (n0 + n) + r;
+        if (col >= d.K) continue;
+        float kv = static_cast<float>(kt[0][n][mt >> 1][(mt & 1) * 4 + e]), qv = static_cast<float>(qt[0][n][mt >> 1][(mt & 1) * 4 + e]);
+        if (NP == 2) {
+          kv += static_cast<float>(kt[NP - 1][n][mt >> 1][(mt & 1) * 4 + e]);
+          qv += static_cast<float>(qt[NP - 1][n][mt >> 1][(mt & 1) * 4 + e]);
         }
         const int64_t o = qk + i * (d.G * d.K) + col;
         IO<A>::st(p.d_q, o, rq * (totQ[mt][n][e] - qv * wq) * pq);
@@ -675,7 +759,6 @@ namespace {
 
 template <Act A, int KP>
 hipError_t launch(const BwdArgs& a, hipStream_t st) {
-  constexpr int NW = 4;
   const Dims& d = a.d;
   const unsigned bh = static_cast<unsigned>(d.B * d.H), nc = static_cast<unsigned>(d.nc);
   hipLaunchKernelGGL((gdelta_dymax_kernel<A>), dim3(bh * nc), dim3(256), 0, st, a);
@@ -683,10 +766,11 @@ hipError_t launch(const BwdArgs& a, hipStream_t st) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(gdelta_dscale_kernel, dim3(bh), dim3(64), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const int ncb = (d.VP / 16 + NW - 1) / NW;
-  hipLaunchKernelGGL((gdelta_bwd_state_kernel<A, KP, NW>), dim3(bh * ncb), dim3(NW * 64), 0, st, a);
+  hipLaunchKernelGGL((gdelta_bwd_state_kernel<A, KP>), dim3(bh * (d.VP / 16)), dim3(64), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL((gdelta_bwd_chunk_kernel<A, KP>), dim3(static_cast<unsigned>(d.B * d.G) * nc), dim3(256), 0, st, a);
+  const dim3 grid(static_cast<unsigned>(d.B * d.G) * nc);
+  if (d.H == d.G) hipLaunchKernelGGL((gdelta_bwd_chunk_kernel<A, KP, false>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((gdelta_bwd_chunk_kernel<A, KP, true>), grid, dim3(256), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(gdelta_params_kernel, dim3(static_cast<unsigned>(d.H)), dim3(256), 0, st, a);
   return hipGetLastError();

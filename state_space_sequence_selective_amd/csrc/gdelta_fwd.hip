@@ -1,17 +1,110 @@
-// Gated delta rule, forward: the per-chunk triangular inverse, the pass over
-// the chunks, and the token-by-token step (gfx950).  The algebra and the
-// number format are in gdelta.h.
+// Gated delta rule, forward: the chunks' operands, the per-chunk triangular
+// inverse, the pass over the chunks, and the token-by-token step (gfx950).
+// The algebra and the number format are in gdelta.h.
 #include <type_traits>
 
 #include "gdelta_launch.h"
 
 namespace gdelta {
 
+// ------------------------------------------------------------------ q and k as operands
+// One workgroup per (batch row, query / key head, chunk): each row's power of two and unit scale, and its f16 parts as
+// fragments, through LDS.
+template <Act A, int KP>
+__global__ void __launch_bounds__(256) gdelta_rows_kernel(const FwdArgs p) {
+  constexpr int NP = A == Act::F32 ? 2 : 1, EPT = KP / 4, ROW = KP + 8, KS = KP / 32;
+  __shared__ __attribute__((aligned(16))) uint16_t s[2][NP][kC * ROW];
+  const Dims& d = p.d;
+  const int tid = threadIdx.x, lane = tid & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
+  const int64_t c = blockIdx.x % d.nc, bg = blockIdx.x / d.nc, hk = bg % d.G, b = bg / d.G;
+  const int64_t t0 = c * kC, left = d.T - t0, ci = bg * d.nc + c;
+  float* sc = p.w.gsc + ci * (kGroupSc * kC);
+  const int row = tid >> 2, part = tid & 3;   // four threads a row
+  const int64_t base = ((b * d.T + t0 + row) * d.G + hk) * d.K;
+  float x[2][EPT];
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int e = 0; e < EPT; e += 8) {
+      const int col = part * EPT + e;
+      load8<A>(which ? p.q : p.k, base + col, row < left && col < d.K, x[which] + e);
+    }
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float m = 0.0f, ss = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) m = max_finite(m, x[which][e]);
+    m = fmaxf(m, __shfl_xor(m, 1, 64));
+    m = fmaxf(m, __shfl_xor(m, 2, 64));
+    const float pw = pow2_below(m, 2);
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      x[which][e] *= pw;
+      ss = fmaf(x[which][e], x[which][e], ss);
+    }
+    ss += __shfl_xor(ss, 1, 64);
+    ss += __shfl_xor(ss, 2, 64);
+    const float rs = unit_scale(ss, pw, d.eps);
+    if (part == 0) {
+      sc[(which ? G_PQ : G_PK) * kC + row] = pw;
+      sc[(which ? G_RQ : G_RK) * kC + row] = which ? rs * d.scale : rs;
+    }
+#pragma unroll
+    for (int e = 0; e < EPT; e += 8) {
+      u32x4 hi, lo;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a, bb;
+        split2(x[which][e + 2 * k], x[which][e + 2 * k + 1], a, bb);
+        hi[k] = a;
+        lo[k] = bb;
+      }
+      *reinterpret_cast<u32x4*>(s[which][0] + row * ROW + part * EPT + e) = hi;
+      if (NP == 2) *reinterpret_cast<u32x4*>(s[which][NP - 1] + row * ROW + part * EPT + e) = lo;
+    }
+  }
+  __syncthreads();
+  constexpr int NF = KP / 8;   // fragments of a plane, of either family
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int pl = 0; pl < NP; ++pl) {
+      const uint16_t* src = s[which][pl];
+      uint16_t* F = (which ? p.w.QF : p.w.KF) + (ci * NP + pl) * (NF * kFrag);
+#pragma unroll
+      for (int i = 0; i < NF / 4; ++i) {
+        const int f = i * 4 + wv, mt = f / KS, ks = f % KS;
+        const uint16_t* a = src + (16 * mt + r) * ROW + 32 * ks + 4 * g;
+        const u32x2 lo = *reinterpret_cast<const u32x2*>(a), hi = *reinterpret_cast<const u32x2*>(a + 16);
+        at<u32x4>(F + f * kFrag, lane * 16) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
+      if (which && !p.w.QT) continue;
+      uint16_t* Tr = (which ? p.w.QT : p.w.KT) + (ci * NP + pl) * (NF * kFrag);
+#pragma unroll
+      for (int i = 0; i < NF / 4; ++i) {
+        const int f = i * 4 + wv, n = f / 2, ks = f % 2;
+        const uint16_t* a = src + (32 * ks + 4 * g) * ROW + 16 * n + r;
+        u32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int x0 = (e & 1) * 2 + (e >> 1) * 16;
+          v[e] = a[x0 * ROW] | (static_cast<uint32_t>(a[(x0 + 1) * ROW]) << 16);
+        }
+        at<u32x4>(Tr + f * kFrag, lane * 16) = v;
+      }
+    }
+}
+
+// y is rounded to its type.  For bf16 (2^-9) one f16 part (2^-12) of P, u and the state is enough in it, and adds
+// about 1% to its error; f16 and f32 take both.  What feeds the state or a gradient has both always.
+template <Act A>
+constexpr int kPPlanes = A == Act::BF16 ? 1 : 2;
+
 // ------------------------------------------------------------------ chunk preparation
-// One workgroup per (batch row, head, chunk): the tokens' gates and unit scales, A = beta k.k^T D in LDS, and its
-// unit lower triangular inverse: four 16 x 16 diagonal blocks by substitution, then two levels of
-// T21 = -T22 (A21 T11) on f32 matrix instructions (v_mfma_f32_16x16x4_f32; full f32, as an inverse amplifies
-// roundings of A).
+// One workgroup per (batch row, head, chunk): the tokens' gates; P = q.k^T D and its transpose, whose fragments are the
+// result tiles of k.q^T and q.k^T as they stand; A = beta k.k^T D in LDS and its unit lower triangular inverse: four
+// 16 x 16 diagonal blocks by substitution, then two levels of T21 = -T22 (A21 T11) on f32 matrix instructions
+// (v_mfma_f32_16x16x4_f32; full f32, as an inverse amplifies roundings of A).
 constexpr int kAS = kC + 4;
 
 __device__ __forceinline__ f32x4 mma32(float a, float b, f32x4 c) {
@@ -32,88 +125,42 @@ __device__ __forceinline__ f32x4 tile_mm(const float* a, f32x4 b, int r, int g, 
   return acc;
 }
 
-// the (row tile, 32-column step) pairs of T and of T^T that hold anything but zeros
-__device__ constexpr int kTm[6] = {0, 1, 2, 2, 3, 3}, kTk[6] = {0, 0, 0, 1, 0, 1};
-__device__ constexpr int kTTm[6] = {0, 0, 1, 1, 2, 3}, kTTk[6] = {0, 1, 0, 1, 1, 1};
-
 template <Act A, int KP>
 __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
-  constexpr int NP = A == Act::F32 ? 2 : 1;
-  constexpr int EPT = KP / 4;   // elements of a row per thread
-  __shared__ __attribute__((aligned(16))) uint16_t sK[NP * kC * kRow<KP>];
+  constexpr int NP = A == Act::F32 ? 2 : 1, KS = KP / 32, NF = KP / 8;
   __shared__ __attribute__((aligned(16))) float sA[kC * kAS], sT[kC * kAS];
   __shared__ double sG[kC];
-  __shared__ float sBeta[kC], sRk[kC], sMax[4];
+  __shared__ float sBeta[kC], sRk[kC], sRq[kC], sMax[4];
   const Dims& d = p.d;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, r = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
   const int64_t c = blockIdx.x % d.nc, bh = blockIdx.x / d.nc, h = bh % d.H, b = bh / d.H, hk = h / (d.H / d.G);
-  const int64_t t0 = c * kC, left = d.T - t0;
-  float* sc = p.w.sc + (bh * d.nc + c) * (kSc * kC);
+  const int64_t t0 = c * kC, left = d.T - t0, ci = bh * d.nc + c, gi = (b * d.G + hk) * d.nc + c;
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   if (tid < kC) {
     const bool ok = tid < left;
     const int64_t i = (b * d.T + t0 + tid) * d.H + h;
     const float rate = exp2_fast(p.a_log[h] * kLog2e);
     double G = ok ? log2_decay(rate, p.a_raw[i], p.dt_bias[h]) : 0.0f;
     const float beta = ok ? mscan::sigmoid(p.b_raw[i]) : 0.0f;
+    const float rk = p.w.gsc[gi * (kGroupSc * kC) + G_RK * kC + tid], rq = p.w.gsc[gi * (kGroupSc * kC) + G_RQ * kC + tid];
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) {
       const double o = __shfl_up(G, s, 64);
       if (lane >= s) G += o;
     }
+    const double Gl = __shfl(G, 63, 64);
     sG[tid] = G;
     sBeta[tid] = beta;
-    p.w.G[(bh * d.nc + c) * kC + tid] = G;
-    sc[SC_BETA * kC + tid] = beta;
-    sc[SC_E * kC + tid] = exp2_fast(static_cast<float>(G));
-  }
-  {
-    const int row = tid >> 2, part = tid & 3;
-    float x[EPT];
-    const int64_t base = ((b * d.T + t0 + row) * d.G + hk) * d.K;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const void* src = which ? p.q : p.k;
-      float m = 0.0f, ss = 0.0f;
-#pragma unroll
-      for (int e = 0; e < EPT; e += 8) {
-        const int col = part * EPT + e;
-        load8<A>(src, base + col, row < left && col < d.K, x + e);
-      }
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) m = max_finite(m, x[e]);
-      m = fmaxf(m, __shfl_xor(m, 1, 64));
-      m = fmaxf(m, __shfl_xor(m, 2, 64));
-      const float pw = pow2_below(m, 2);
-#pragma unroll
-      for (int e = 0; e < EPT; ++e) {
-        x[e] *= pw;
-        ss = fmaf(x[e], x[e], ss);
-      }
-      ss += __shfl_xor(ss, 1, 64);
-      ss += __shfl_xor(ss, 2, 64);
-      const float rs = unit_scale(ss, pw, d.eps);
-      if (which == 0) {
-#pragma unroll
-        for (int e = 0; e < EPT; e += 8) {
-          u32x4 hi, lo;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t a, bb;
-            split2(x[e + 2 * k], x[e + 2 * k + 1], a, bb);
-            hi[k] = a;
-            lo[k] = bb;
-          }
-          uint16_t* dst = sK + row * kRow<KP> + part * EPT + e;
-          *reinterpret_cast<u32x4*>(dst) = hi;
-          if (NP == 2) *reinterpret_cast<u32x4*>(dst + kC * kRow<KP>) = lo;
-        }
-      }
-      if (part == 0) {
-        if (which == 0) sRk[row] = rs;
-        sc[(which ? SC_PQ : SC_PK) * kC + row] = pw;
-        sc[(which ? SC_RQ : SC_RK) * kC + row] = which ? rs * d.scale : rs;
-      }
-    }
+    sRk[tid] = rk;
+    sRq[tid] = rq * d.pscale;
+    p.w.G[ci * kC + tid] = G;
+    float* sc = p.w.hsc + ci * (kHeadSc * kC);
+    const float e = exp2_fast(static_cast<float>(G));
+    sc[H_BETA * kC + tid] = beta;
+    sc[H_E * kC + tid] = e;
+    sc[H_BK * kC + tid] = beta * e * rk;
+    sc[H_DK * kC + tid] = exp2_fast(static_cast<float>(Gl - G)) * rk;
+    sc[H_EQ * kC + tid] = e * rq;
   }
   // the largest |v|, and the initial state's bound sqrt(d_k) max |h0|
   float m = 0.0f;
@@ -135,24 +182,66 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
     if (lane == 0) sMax[wv] = m;
   }
   __syncthreads();
-  if (tid == 0) p.w.vmax[bh * d.nc + c] = fmaxf(fmaxf(sMax[0], sMax[1]), fmaxf(sMax[2], sMax[3]));
-  for (int nt = 0; nt <= wv; ++nt) {
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (tid == 0) p.w.vmax[ci] = fmaxf(fmaxf(sMax[0], sMax[1]), fmaxf(sMax[2], sMax[3]));
+  const uint16_t* KF = p.w.KF + gi * (NP * NF * kFrag);
+  const uint16_t* QF = p.w.QF + gi * (NP * NF * kFrag);
+  {
+    // wave w: tiles (rows j of tile n, columns i of tile w), n <= w
+    const int i = 16 * wv + r;
+    const float rki = sRk[i], rqi = sRq[i], be = sBeta[i];
+    const double Gi = sG[i];
+    f32x4 P[4];
 #pragma unroll
-    for (int ks = 0; ks < KP / 32; ++ks) {
-      const uint16_t* pa = sK + (16 * wv + r) * kRow<KP> + 32 * ks + 8 * g;
-      const uint16_t* pb = sK + (16 * nt + r) * kRow<KP> + 32 * ks + 8 * g;
-      acc = mma(ld8(pa), ld8(pb), acc);
-      if (NP == 2) {
-        acc = mma(ld8(pa), ld8(pb + kC * kRow<KP>), acc);
-        acc = mma(ld8(pa + kC * kRow<KP>), ld8(pb), acc);
+    for (int n = 0; n < 4; ++n) {
+      P[n] = zero;
+      if (n > wv) continue;
+      const f32x4 kk = frag_mm<NP, KS, NF>(KF + n * KS * kFrag, KF + wv * KS * kFrag, lane, zero);
+      const f32x4 kq = frag_mm<NP, KS, NF>(KF + n * KS * kFrag, QF + wv * KS * kFrag, lane, zero);
+      f32x4 a;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = 16 * n + 4 * g + e;
+        const float w = j <= i ? sRk[j] * exp2_fast(static_cast<float>(Gi - sG[j])) : 0.0f;
+        P[n][e] = rqi * w * kq[e];
+        a[e] = j < i ? be * rki * w * kk[e] : 0.0f;
+      }
+      *reinterpret_cast<f32x4*>(sA + i * kAS + 16 * n + 4 * g) = a;
+    }
+    constexpr int PP = kPPlanes<A>;
+    uint16_t* dst = p.w.P + ci * (PP * 6 * kFrag);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      if (ks == 1 && wv < 2) continue;
+      const int f = wv < 2 ? wv : 2 * wv - 2 + ks;
+      const Frag x = to_b(P[2 * ks], P[2 * ks + 1]);
+      at<h8>(dst + f * kFrag, lane * 16) = x.hi;
+      if (PP == 2) at<h8>(dst + (6 + f) * kFrag, lane * 16) = x.lo;
+    }
+  }
+  if (p.w.PT) {   // wave w: tiles (rows i of tile n, columns j of tile w), n >= w
+    const int j = 16 * wv + r;
+    const float rkj = sRk[j];
+    const double Gj = sG[j];
+    f32x4 P[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      P[n] = zero;
+      if (n < wv) continue;
+      const f32x4 qk = frag_mm<NP, KS, NF>(QF + n * KS * kFrag, KF + wv * KS * kFrag, lane, zero);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * n + 4 * g + e;
+        P[n][e] = j <= i ? sRq[i] * rkj * exp2_fast(static_cast<float>(sG[i] - Gj)) * qk[e] : 0.0f;
       }
     }
-    const int j = 16 * nt + r;
+    uint16_t* dst = p.w.PT + ci * (2 * 6 * kFrag);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = 16 * wv + 4 * g + e;
-      sA[i * kAS + j] = j < i ? sBeta[i] * (sRk[i] * sRk[j]) * acc[e] * exp2_fast(static_cast<float>(sG[i] - sG[j])) : 0.0f;
+    for (int ks = 0; ks < 2; ++ks) {
+      if (ks == 0 && wv >= 2) continue;
+      const int f = wv < 2 ? 2 * wv + ks : 2 + wv;
+      const Frag x = to_b(P[2 * ks], P[2 * ks + 1]);
+      at<h8>(dst + f * kFrag, lane * 16) = x.hi;
+      at<h8>(dst + (6 + f) * kFrag, lane * 16) = x.lo;
     }
   }
   __syncthreads();
@@ -171,10 +260,8 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
   __syncthreads();
   if (wv < 2) {    // blocks (1, 0) and (3, 2)
     const int o = 32 * wv;
-    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-    x = tile_mm(sA + (o + 16) * kAS + o, sT + o * kAS + o, r, g, x);
-    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-    y = tile_mm(sT + (o + 16) * kAS + o + 16, x, r, g, y);
+    const f32x4 x = tile_mm(sA + (o + 16) * kAS + o, sT + o * kAS + o, r, g, zero);
+    const f32x4 y = tile_mm(sT + (o + 16) * kAS + o + 16, x, r, g, zero);
 #pragma unroll
     for (int e = 0; e < 4; ++e) sT[(o + 16 + 4 * g + e) * kAS + o + r] = -y[e];
   }
@@ -183,13 +270,13 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
     f32x4 x[2];
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi) {
-      x[mi] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      x[mi] = zero;
       for (int kk = wv; kk < 2; ++kk)
         x[mi] = tile_mm(sA + (32 + 16 * mi) * kAS + 16 * kk, sT + 16 * kk * kAS + 16 * wv, r, g, x[mi]);
     }
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi) {
-      f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+      f32x4 y = zero;
 #pragma unroll
       for (int kk = 0; kk <= mi; ++kk) y = tile_mm(sT + (32 + 16 * mi) * kAS + 32 + 16 * kk, x[kk], r, g, y);
 #pragma unroll
@@ -197,12 +284,12 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
     }
   }
   __syncthreads();
-  uint16_t* T = p.w.T + (bh * d.nc + c) * (kTFrag * 512);
-  uint16_t* TT = p.w.TT ? p.w.TT + (bh * d.nc + c) * (kTFrag * 512) : nullptr;
+  uint16_t* T = p.w.T + ci * (12 * kFrag);
+  uint16_t* TT = p.w.TT ? p.w.TT + ci * (12 * kFrag) : nullptr;
   for (int it = tid; it < 2 * 6 * 64; it += 256) {
     const bool tr = it >= 6 * 64;
     if (tr && !TT) break;
-    const int f = (it >> 6) % 6, i = 16 * (tr ? kTTm[f] : kTm[f]) + r, k0 = 32 * (tr ? kTTk[f] : kTk[f]);
+    const int f = (it >> 6) % 6, i = 16 * (tr ? kUm[f] : kLm[f]) + r, k0 = 32 * (tr ? kUk[f] : kLk[f]);
     u32x4 hi, lo;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -217,53 +304,47 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
       hi[e] = a;
       lo[e] = bb;
     }
-    uint16_t* dst = (tr ? TT : T) + (f * 64 + lane) * 8;
+    uint16_t* dst = (tr ? TT : T) + f * kFrag + lane * 8;
     *reinterpret_cast<u32x4*>(dst) = hi;
-    *reinterpret_cast<u32x4*>(dst + 6 * 512) = lo;
+    *reinterpret_cast<u32x4*>(dst + 6 * kFrag) = lo;
   }
 }
 
 // ------------------------------------------------------------------ pass over the chunks
 // A wave holds 16 columns of one head's S^T (rows: d_k) in registers, as the accumulators of the state update; they
-// are at once the B operand of the products with k and q, and u is one for the update, so a wave's chain needs no
-// exchange with other waves.  The workgroup's waves share k, q and the masked q.k^T in LDS.
-template <Act A, int KP, int NW>
-struct FwdLds {
-  static constexpr int NP = A == Act::F32 ? 2 : 1;
-  uint16_t k[NP * kC * kRow<KP>];
-  uint16_t q[NP * kC * kRow<KP>];
-  uint16_t kT[NP * KP * kCol];
-  uint16_t P[2 * kC * kCol];
-  double G[kC];
-  float beta[kC], ek[kC], eq[kC], dk[kC], rk[kC], rq[kC];
-};
-
-template <Act A, int KP, int NW, bool SAVE>
-__global__ void __launch_bounds__(NW * 64) gdelta_fwd_kernel(const FwdArgs p) {
-  constexpr int NP = A == Act::F32 ? 2 : 1, MT = KP / 16, KS = KP / 32;
-  __shared__ __attribute__((aligned(16))) FwdLds<A, KP, NW> s;
-  static_assert(sizeof(s) <= mscan::kLdsBytes, "LDS");
-  const Dims& d = p.d;
-  const int tid = threadIdx.x, lane = tid & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
-  const int ncb = (d.VP / 16 + NW - 1) / NW;
-  const int64_t bh = blockIdx.x / ncb, h = bh % d.H, b = bh / d.H, hk = h / (d.H / d.G);
-  const int col = ((blockIdx.x % ncb) * NW + wv) * 16 + r;
-  const bool ok = col < d.V, live = col < d.VP;
+// are at once the B operand of the products with k and q, and u is one for the update, so a wave needs nothing of any
+// other: no LDS but for its tokens' scalars, no barrier.  The next chunk's fragments are loaded as soon as this one's
+// are used.
+template <Act A, int KP, bool SAVE>
+__global__ void __launch_bounds__(64) gdelta_fwd_kernel(const FwdArgs p) {
+  constexpr int NP = A == Act::F32 ? 2 : 1, MT = KP / 16, KS = KP / 32, NF = KP / 8, PP = kPPlanes<A>;
+  constexpr bool AHEAD = NP == 1;   // two planes do not fit the registers: loaded where they are used
   using Raw = std::conditional_t<A == Act::F32, uint32_t, uint16_t>;
   constexpr int ES = sizeof(Raw);
-  const uint32_t vrow = static_cast<uint32_t>(d.H) * d.V * ES, vcol = ok ? col : d.V - 1;   // bytes of a token's v; a column to read
-  const uint32_t poff = (4 * g * d.VP + col) * 4;   // this lane's place in the packed S and U
+  __shared__ __attribute__((aligned(16))) float s[4][kC];   // beta; beta e rk; exp(G_63 - G) rk; e rq
+  const Dims& d = p.d;
+  const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
+  int64_t bh;
+  int cb;
+  xcd_head(blockIdx.x, d.VP / 16, d.B * d.H, bh, cb);
+  const int64_t h = bh % d.H, b = bh / d.H, hk = h / (d.H / d.G), bg = b * d.G + hk;
+  const int col = cb * 16 + r;
+  const bool ok = col < d.V;
+  const uint32_t vrow = static_cast<uint32_t>(d.H) * d.V * ES;   // bytes of a token's v
+  const uint32_t voff = vrow * 4 * g + (ok ? col : d.V - 1) * ES, yoff = vrow * 4 * g + col * ES;
+  const uint32_t poff = (4 * g * d.VP + col) * 4;                // this lane's place in the packed S and U
   // the head's power of two: |s|, |v - S k| <= 2 sqrt(T + 1) max(|v|, |h0|) scaled below 2^15
   float m = 0.0f;
   for (int64_t i = lane; i < d.nc; i += 64) m = fmaxf(m, p.w.vmax[bh * d.nc + i]);
   const float sv = pow2_below(wave_max(m), 15 - static_cast<int>(ceilf(1.0f + 0.5f * log2f(static_cast<float>(d.T) + 1.0f))));
   const float rsv = 1.0f / sv, rps = 1.0f / d.pscale, svc = ok ? sv : 0.0f;
-  if (SAVE && tid == 0 && blockIdx.x % ncb == 0) p.w.sv[bh] = sv;
+  if (SAVE && lane == 0 && cb == 0) p.w.sv[bh] = sv;
 
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   f32x4 S[MT];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    S[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    S[mt] = zero;
     const int row = 16 * mt + 4 * g;
     if (p.h0 && ok && row < d.K) {
       const f32x4 x = *reinterpret_cast<const f32x4*>(p.h0 + (bh * d.V + col) * d.K + row);
@@ -271,174 +352,170 @@ __global__ void __launch_bounds__(NW * 64) gdelta_fwd_kernel(const FwdArgs p) {
       for (int e = 0; e < 4; ++e) S[mt][e] = x[e] * sv;
     }
   }
-  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  // what the next chunk reads, in flight while this one computes
-  QkRegs<A, KP, NW * 64> qk;
-  h8 th[6], tl[6];
-  float scal[4];       // beta, e, rk, rq of token `lane`
-  double G, Gl;
+  h8 kf[NF], qf[NF], kt[NF], pf[6], th[6], tl[6];
+  float sc[4], el;
   uint32_t v[4][4];
-  auto load_chunk = [&](int64_t c) {
-    const int64_t t0 = c * kC, ci = bh * d.nc + c;
-    const float* sc = p.w.sc + ci * (kSc * kC);
-    qk.load(p.k, p.q, ((b * d.T + t0) * d.G + hk) * d.K, d.G * d.K, d.K, d.T - t0, sc, tid);
-    G = p.w.G[ci * kC + lane];
-    Gl = p.w.G[ci * kC + kC - 1];
-    scal[0] = sc[SC_BETA * kC + lane];
-    scal[1] = sc[SC_E * kC + lane];
-    scal[2] = sc[SC_RK * kC + lane];
-    scal[3] = sc[SC_RQ * kC + lane];
-  };
-  auto load_t = [&](int64_t c) {
-    const uint16_t* T = p.w.T + (bh * d.nc + c) * (kTFrag * 512);
+  auto frags = [&](h8* x, const uint16_t* base, int n) {
 #pragma unroll
-    for (int f = 0; f < 6; ++f) {
-      th[f] = at<h8>(T + f * 512, lane * 16);
-      tl[f] = at<h8>(T + (6 + f) * 512, lane * 16);
-    }
+    for (int i = 0; i < n; ++i) x[i] = at<h8>(base + i * kFrag, lane * 16);
+  };
+  auto KFp = [&](int64_t c) { return p.w.KF + (bg * d.nc + c) * (NP * NF * kFrag); };
+  auto QFp = [&](int64_t c) { return p.w.QF + (bg * d.nc + c) * (NP * NF * kFrag); };
+  auto KTp = [&](int64_t c) { return p.w.KT + (bg * d.nc + c) * (NP * NF * kFrag); };
+  auto Pp = [&](int64_t c) { return p.w.P + (bh * d.nc + c) * (PP * 6 * kFrag); };
+  auto Tp = [&](int64_t c) { return p.w.T + (bh * d.nc + c) * (12 * kFrag); };
+  auto load_t = [&](int64_t c) {
+    frags(th, Tp(c), 6);
+    frags(tl, Tp(c) + 6 * kFrag, 6);
+  };
+  auto load_sc = [&](int64_t c) {
+    const float* x = p.w.hsc + (bh * d.nc + c) * (kHeadSc * kC);
+    sc[0] = x[H_BETA * kC + lane];
+    sc[1] = x[H_BK * kC + lane];
+    sc[2] = x[H_DK * kC + lane];
+    sc[3] = x[H_EQ * kC + lane];
+    el = x[H_E * kC + kC - 1];
   };
   auto load_v = [&](int64_t c) {
     const int64_t left = d.T - c * kC;
     const char* base = static_cast<const char*>(p.v) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES);
-    const uint32_t off = vrow * 4 * g + vcol * ES;
     const int64_t row = fresh(vrow);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         v[mt][e] = 0u;
-        if (left >= kC || 16 * mt + 4 * g + e < left) v[mt][e] = at<Raw>(base + (16 * mt + e) * row, off);
+        if (left >= kC || 16 * mt + 4 * g + e < left) v[mt][e] = at<Raw>(base + (16 * mt + e) * row, voff);
       }
   };
-  load_chunk(0);
-  load_t(0);
+  if (AHEAD) {
+    frags(kf, KFp(0), NF);
+    frags(qf, QFp(0), NF);
+    load_t(0);
+    frags(kt, KTp(0), NF);
+    frags(pf, Pp(0), 6);
+  }
+  load_sc(0);
   load_v(0);
   for (int64_t c = 0; c < d.nc; ++c) {
-    const int64_t t0 = c * kC, left = d.T - t0, ci = bh * d.nc + c;
-    mscan::lds_barrier();   // the previous chunk's readers are done
-    qk.store(s.k, s.q, s.kT, nullptr, tid);
-    if (wv == 0) {
-      s.G[lane] = G;
-      s.beta[lane] = scal[0];
-      s.ek[lane] = scal[1] * scal[2];
-      s.eq[lane] = scal[1] * scal[3];
-      s.dk[lane] = exp2_fast(static_cast<float>(Gl - G)) * scal[2];
-      s.rk[lane] = scal[2];
-      s.rq[lane] = scal[3] * d.pscale;
+    const int64_t left = d.T - c * kC, ci = bh * d.nc + c;
+    const bool more = AHEAD && c + 1 < d.nc;
+    mscan::wave_lds_sync();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i][lane] = sc[i];
+    mscan::wave_lds_sync();
+    const float elc = el;
+    if (c + 1 < d.nc) load_sc(c + 1);
+    if (!AHEAD) {
+      frags(kf, KFp(c), NF);
+      frags(qf, QFp(c), NF);
     }
-    const float el = exp2_fast(static_cast<float>(Gl));
-    if (c + 1 < d.nc) load_chunk(c + 1);
-    mscan::lds_barrier();
-    // P = q.k^T D on and below the diagonal, zeros in the two tiles above it that a 32-wide step reads
-#pragma unroll
-    for (int n = 0; n < (12 + NW - 1) / NW; ++n) {
-      const int i = wv + n * NW;
-      if (12 % NW && i >= 12) break;
-      const int mt = i < 2 ? 0 : i < 4 ? 1 : i < 8 ? 2 : 3, nt = i - (i < 2 ? 0 : i < 4 ? 2 : i < 8 ? 4 : 8);
-      f32x4 acc = zero;
-      if (nt <= mt) {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint16_t* pa = s.q + (16 * mt + r) * kRow<KP> + 32 * ks + 8 * g;
-          const uint16_t* pb = s.k + (16 * nt + r) * kRow<KP> + 32 * ks + 8 * g;
-          acc = mma(ld8(pa), ld8(pb), acc);
-          if (NP == 2) {
-            acc = mma(ld8(pa), ld8(pb + kC * kRow<KP>), acc);
-            acc = mma(ld8(pa + kC * kRow<KP>), ld8(pb), acc);
-          }
-        }
-      }
-      const int j = 16 * nt + r;
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        float x[2];
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          const int row = 16 * mt + 4 * g + e + o;
-          x[o] = j <= row ? s.rq[row] * s.rk[j] * acc[e + o] * exp2_fast(static_cast<float>(s.G[row] - s.G[j])) : 0.0f;
-        }
-        uint32_t hi, lo;
-        split2(x[0], x[1], hi, lo);
-        uint16_t* dst = s.P + (16 * mt + 4 * g + e) * kCol + place(j);
-        dst[0] = static_cast<uint16_t>(hi);
-        dst[kCol] = static_cast<uint16_t>(hi >> 16);
-        dst[kC * kCol] = static_cast<uint16_t>(lo);
-        dst[kC * kCol + kCol] = static_cast<uint16_t>(lo >> 16);
-      }
-    }
-
     f32x4 ak[4], aq[4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) ak[mt] = aq[mt] = zero;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const Frag f = to_b(S[2 * ks], S[2 * ks + 1]);
-      if (SAVE && live) store_packed(p.w.S + (ci * KP + 32 * ks) * d.VP, poff, f, d.VP);
+      if (SAVE) store_packed(p.w.S + (ci * KP + 32 * ks) * d.VP, poff, f, d.VP);
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        const int at = (16 * mt + r) * kRow<KP> + 32 * ks + 8 * g;
-        ak[mt] = mma_split<NP>(s.k + at, kC * kRow<KP>, f, ak[mt]);
-        aq[mt] = mma_split<NP>(s.q + at, kC * kRow<KP>, f, aq[mt]);
+      for (int mt = 0; mt < 4; ++mt) ak[mt] = mma(kf[mt * KS + ks], f.hi, ak[mt]);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) ak[mt] = mma(kf[mt * KS + ks], f.lo, ak[mt]);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) aq[mt] = mma(qf[mt * KS + ks], f.hi, aq[mt]);
+      if (PP == 2) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) aq[mt] = mma(qf[mt * KS + ks], f.lo, aq[mt]);
       }
+      if (NP == 2) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+          ak[mt] = mma(at<h8>(KFp(c) + (NF + mt * KS + ks) * kFrag, lane * 16), f.hi, ak[mt]);
+          aq[mt] = mma(at<h8>(QFp(c) + (NF + mt * KS + ks) * kFrag, lane * 16), f.hi, aq[mt]);
+        }
+      }
+    }
+    if (more) {
+      frags(kf, KFp(c + 1), NF);
+      frags(qf, QFp(c + 1), NF);
     }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      const f32x4 be = *reinterpret_cast<const f32x4*>(s.beta + 16 * mt + 4 * g), ek = *reinterpret_cast<const f32x4*>(s.ek + 16 * mt + 4 * g);
+      const f32x4 be = *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * g), bk = *reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * g);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ak[mt][e] = be[e] * (IO<A>::cvt(v[mt][e]) * svc - ek[e] * ak[mt][e]);
+      for (int e = 0; e < 4; ++e) ak[mt][e] = fmaf(be[e], IO<A>::cvt(v[mt][e]) * svc, -bk[e] * ak[mt][e]);
+    }
+    if (c + 1 < d.nc) load_v(c + 1);
+    if (!AHEAD) {
+      load_t(c);
+      frags(kt, KTp(c), NF);
+      frags(pf, Pp(c), 6);
     }
     const Frag x0 = to_b(ak[0], ak[1]), x1 = to_b(ak[2], ak[3]);
     f32x4 U[4] = {zero, zero, zero, zero};
 #pragma unroll
-    for (int f = 0; f < 6; ++f) {
-      const Frag& x = kTk[f] ? x1 : x0;
-      f32x4 a = U[kTm[f]];
-      a = mma(th[f], x.hi, a);
-      a = mma(th[f], x.lo, a);
-      U[kTm[f]] = mma(tl[f], x.hi, a);
-    }
-    if (c + 1 < d.nc) {
-      load_v(c + 1);
-      load_t(c + 1);
-    }
+    for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(th[f], (kLk[f] ? x1 : x0).hi, U[kLm[f]]);
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(th[f], (kLk[f] ? x1 : x0).lo, U[kLm[f]]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) U[mt][e] *= 1.0f / kTScale;
+    for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(tl[f], (kLk[f] ? x1 : x0).hi, U[kLm[f]]);
+    if (more) load_t(c + 1);
+    f32x4 D[4];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      const f32x4 dk = *reinterpret_cast<const f32x4*>(s[2] + 16 * mt + 4 * g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        U[mt][e] *= 1.0f / kTScale;
+        D[mt][e] = U[mt][e] * dk[e];
+      }
+    }
+    const Frag d0 = to_b(D[0], D[1]), d1 = to_b(D[2], D[3]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[mt][e] *= elc;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(kt[2 * mt], d0.hi, S[mt]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(kt[2 * mt], d0.lo, S[mt]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(kt[2 * mt + 1], d1.hi, S[mt]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(kt[2 * mt + 1], d1.lo, S[mt]);
+    if (NP == 2) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        S[mt] = mma(at<h8>(KTp(c) + (NF + 2 * mt) * kFrag, lane * 16), d0.hi, S[mt]);
+        S[mt] = mma(at<h8>(KTp(c) + (NF + 2 * mt + 1) * kFrag, lane * 16), d1.hi, S[mt]);
+      }
+    }
+    if (more) frags(kt, KTp(c + 1), NF);
     const Frag u0 = to_b(U[0], U[1]), u1 = to_b(U[2], U[3]);
-    if (SAVE && live) {
+    if (SAVE) {
       store_packed(p.w.U + ci * kC * d.VP, poff, u0, d.VP);
       store_packed(p.w.U + (ci * kC + 32) * d.VP, poff, u1, d.VP);
     }
+    f32x4 y[4] = {zero, zero, zero, zero};
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      const f32x4 dk = *reinterpret_cast<const f32x4*>(s.dk + 16 * mt + 4 * g);
+    for (int f = 0; f < 6; ++f) y[kLm[f]] = mma(pf[f], (kLk[f] ? u1 : u0).hi, y[kLm[f]]);
+    if (PP == 2) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) U[mt][e] *= dk[e];
+      for (int f = 0; f < 6; ++f) {
+        y[kLm[f]] = mma(pf[f], (kLk[f] ? u1 : u0).lo, y[kLm[f]]);
+        y[kLm[f]] = mma(at<h8>(Pp(c) + (6 + f) * kFrag, lane * 16), (kLk[f] ? u1 : u0).hi, y[kLm[f]]);
+      }
     }
-    const Frag d0 = to_b(U[0], U[1]), d1 = to_b(U[2], U[3]);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[mt][e] *= el;
-      const uint16_t* a = s.kT + (16 * mt + r) * kCol + 8 * g;
-      S[mt] = mma_split<NP>(a, KP * kCol, d0, S[mt]);
-      S[mt] = mma_split<NP>(a + 32, KP * kCol, d1, S[mt]);
-    }
-    mscan::lds_barrier();   // all of P
-    char* y = static_cast<char*>(p.y) + ((b * d.T + t0) * d.H + h) * (d.V * ES);
-    const uint32_t yoff = vrow * 4 * g + col * ES;
+    if (more) frags(pf, Pp(c + 1), 6);
+    char* out = static_cast<char*>(p.y) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES);
     const int64_t yrow = fresh(vrow);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      f32x4 a = zero;
-      a = mma_split<2>(s.P + (16 * mt + r) * kCol + 8 * g, kC * kCol, u0, a);
-      if (mt >= 2) a = mma_split<2>(s.P + (16 * mt + r) * kCol + 32 + 8 * g, kC * kCol, u1, a);
-      const f32x4 eq = *reinterpret_cast<const f32x4*>(s.eq + 16 * mt + 4 * g);
+      const f32x4 eq = *reinterpret_cast<const f32x4*>(s[3] + 16 * mt + 4 * g);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (ok && (left >= kC || 16 * mt + 4 * g + e < left))
-          IO<A>::st(&at<char>(y + (16 * mt + e) * yrow, yoff), 0, (eq[e] * aq[mt][e] + a[e] * rps) * rsv);
+          IO<A>::st(&at<char>(out + (16 * mt + e) * yrow, yoff), 0, fmaf(eq[e], aq[mt][e], y[mt][e] * rps) * rsv);
     }
   }
   if (p.h_last && ok) {
@@ -576,23 +653,24 @@ __global__ void __launch_bounds__(256) gdelta_step_kernel(const FwdArgs p) {
 // ------------------------------------------------------------------ launches
 namespace {
 
-template <Act A, int KP, bool SAVE>
-hipError_t launch_chunks(const FwdArgs& a, hipStream_t st) {
-  constexpr int NW = 4;
+template <Act A, int KP>
+hipError_t launch_chunks(const FwdArgs& a, bool save, hipStream_t st) {
   const Dims& d = a.d;
-  const int64_t bh = d.B * d.H;
-  hipLaunchKernelGGL((gdelta_prep_kernel<A, KP>), dim3(static_cast<unsigned>(bh * d.nc)), dim3(256), 0, st, a);
-  const hipError_t e = hipGetLastError();
+  const unsigned bh = static_cast<unsigned>(d.B * d.H), nc = static_cast<unsigned>(d.nc);
+  hipLaunchKernelGGL((gdelta_rows_kernel<A, KP>), dim3(static_cast<unsigned>(d.B * d.G) * nc), dim3(256), 0, st, a);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int ncb = (d.VP / 16 + NW - 1) / NW;
-  hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, NW, SAVE>), dim3(static_cast<unsigned>(bh * ncb)), dim3(NW * 64), 0, st, a);
+  hipLaunchKernelGGL((gdelta_prep_kernel<A, KP>), dim3(bh * nc), dim3(256), 0, st, a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const dim3 grid(bh * (d.VP / 16));
+  if (save) hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, true>), grid, dim3(64), 0, st, a);
+  else hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, false>), grid, dim3(64), 0, st, a);
   return hipGetLastError();
 }
 
 template <Act A>
 hipError_t launch_act(const FwdArgs& a, bool save, hipStream_t st) {
-  if (a.d.K <= 64) return save ? launch_chunks<A, 64, true>(a, st) : launch_chunks<A, 64, false>(a, st);
-  return save ? launch_chunks<A, 128, true>(a, st) : launch_chunks<A, 128, false>(a, st);
+  return a.d.K <= 64 ? launch_chunks<A, 64>(a, save, st) : launch_chunks<A, 128>(a, save, st);
 }
 
 template <Act A>

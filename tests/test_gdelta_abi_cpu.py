@@ -120,13 +120,17 @@ def test_sizes(pkg):
 
 
 def test_layout(pkg):
-    """16 chunk-heads (2 batch rows, 4 heads, 2 chunks of 64 tokens), piece by piece."""
+    """16 chunk-heads and 8 chunk-groups (2 batch rows, 4 heads of 2 groups, 2 chunks of 64 tokens), piece by piece."""
     al = lambda b: (b + 255) // 256 * 256
-    chunks = 2 * 4 * 2
-    kept = al(chunks * 6 * 64 * 4) + al(chunks * 64 * 8) + al(chunks * 12 * 1024) + al(chunks * 4) + al(8 * 4)
-    assert pkg.gdelta_saved_bytes(gd(pkg)) == kept + al(chunks * 12 * 1024) + 2 * al(chunks * 64 * 32 * 4)
-    bwd = al(chunks * 4) + al(8 * 4) + al(chunks * 8) + 2 * al(chunks * 64 * 32 * 4)
-    assert pkg.gdelta_workspace_bytes(gd(pkg)) == max(kept, bwd)
+    heads, groups, tri = 16, 8, 16 * 6 * 1024
+    for act, planes in (("bf16", 1), ("f32", 2)):
+        family = al(groups * planes * 8 * 1024)      # d_k 64: 8 fragments of 1 KB a plane
+        fwd = (al(groups * 4 * 64 * 4) + 3 * family + al(heads * 5 * 64 * 4) + al(heads * 64 * 8) + al(planes * tri) + al(2 * tri)
+               + al(heads * 4) + al(8 * 4))
+        saved = fwd + family + 2 * al(2 * tri) + 2 * al(heads * 64 * 32 * 4)
+        bwd = al(heads * 4) + al(8 * 4) + al(heads * 8) + 2 * al(heads * 64 * 32 * 4)
+        assert pkg.gdelta_saved_bytes(gd(pkg, act=act)) == saved
+        assert pkg.gdelta_workspace_bytes(gd(pkg, act=act)) == max(fwd, bwd)
     assert pkg.layernorm_workspace_bytes(ln(pkg, rows=5000, dim=5120)) == 1024 * 2 * 5120 * 4
 
 
