@@ -56,9 +56,6 @@ struct Dims {
   float pscale;             // power of two that P = q.k^T D is kept times (|P| <= |scale|)
 };
 
-// T's entries are at most 1: its f16 parts are kept times this, as small ones would lose bits below 2^-24
-constexpr float kTScale = 4096.0f;
-
 // The (row tile, 32-column step) pairs of a lower triangular 64 x 64 matrix that hold anything but zeros, and those of
 // its transpose: six fragments each
 __device__ constexpr int kLm[6] = {0, 1, 2, 2, 3, 3}, kLk[6] = {0, 0, 0, 1, 0, 1};
@@ -79,7 +76,7 @@ struct Kept {
   double* G;        // [64] log2 of the decay since the chunk's start
   uint16_t* P;      // [1 for bf16, else 2][6] lower triangle of q.k^T D, times pscale
   uint16_t* PT;     // [2][6] its transpose (backward)
-  uint16_t* T;      // [2][6] the inverse, times kTScale
+  uint16_t* T;      // [2][6] the inverse (its diagonal is 1, so parts below f16's 2^-24 do not matter)
   uint16_t* TT;     // [2][6] its transpose (backward)
   float* vmax;      // largest finite |v| of the chunk (the first chunk's entry also holds the initial state's bound)
   float* sv;        // [B * H] the head's power of two for S and u
@@ -126,14 +123,16 @@ __device__ __forceinline__ constexpr int place(int x) {
   return (x & ~31) + ((x & 15) >> 2) * 8 + ((x >> 4) & 1) * 4 + (x & 3);
 }
 
-// f32 pair -> packed f16 high parts and packed f16 remainders, both rounded to nearest (v_cvt_pk_f16_f32; the remainder
-// is exact in f32)
+// f32 pair -> packed f16 high parts and packed f16 remainders, both rounded to nearest (v_cvt_pk_f16_f32).  The
+// remainder is exact in f32; v_fma_mix_f32 takes the f16 part as it is (a - h in one instruction).
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const h2 h = __builtin_convertvector((f32x2{a, b}), h2);
-  hi = __builtin_bit_cast(uint32_t, h);
-  lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a - static_cast<float>(h[0]), b - static_cast<float>(h[1])}), h2));
+  hi = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), h2));
+  float x, y;
+  asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(x) : "v"(hi), "v"(a));
+  asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(y) : "v"(hi), "v"(b));
+  lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x, y}), h2));
 }
 
 struct Frag {
@@ -150,14 +149,6 @@ __device__ __forceinline__ const T& at(const void* base, uint32_t off) {
   return *reinterpret_cast<const T*>(static_cast<const char*>(base) + off);
 }
 
-// The value, as something the compiler cannot carry out of a loop: multiples of a row length are cheaper to make again
-// than to keep, one pair of scalar registers each
-__device__ __forceinline__ int64_t fresh(int64_t x) {
-  int lo = __builtin_amdgcn_readfirstlane(static_cast<int>(x));
-  asm volatile("" : "+s"(lo));
-  return lo;
-}
-
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // two stacked D tiles as a split B operand
@@ -171,16 +162,33 @@ __device__ __forceinline__ Frag to_b(f32x4 a, f32x4 b) {
   return {__builtin_bit_cast(h8, hi), __builtin_bit_cast(h8, lo)};
 }
 
-// Stores a split operand's parts as f16 high | low << 16 words to its 4 + 4 rows 4 g + e, 16 + 4 g + e of `rows` words;
+// Buffer instructions: base in scalar registers, a 32-bit byte offset of the lane, one of the wave, and a constant.  Every
+// access here is inside its array; the descriptor's own range check is not relied on.
+using Buf = __amdgpu_buffer_rsrc_t;
+__device__ __forceinline__ Buf buf_of(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, 0x7fffffff, 0x00027000);
+}
+__device__ __forceinline__ h8 buf_h8(Buf b, int lane_off, int wave_off) {
+  return __builtin_bit_cast(h8, __builtin_amdgcn_raw_buffer_load_b128(b, lane_off, wave_off, 0));
+}
+// n fragments of 1 KB from the buffer's base
+template <int N>
+__device__ __forceinline__ void load_frags(h8 (&x)[N], const void* base, int lane) {
+  const Buf b = buf_of(base);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = buf_h8(b, lane * 16 + (i & 3) * 1024, (i >> 2) * 4096);
+}
+
+// Stores a split operand's parts as f16 high | low << 16 words to its 4 + 4 rows 4 g + e, 16 + 4 g + e of `words` words;
 // off: the lane's byte offset in the first of them
-__device__ __forceinline__ void store_packed(uint32_t* base, uint32_t off, const Frag& f, int64_t rows_) {
-  const int64_t rows = fresh(rows_);
+__device__ __forceinline__ void store_packed(uint32_t* base, int off, const Frag& f, int words) {
   const u32x4 hi = __builtin_bit_cast(u32x4, f.hi), lo = __builtin_bit_cast(u32x4, f.lo);
+  const Buf b = buf_of(base);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    uint32_t* q = base + ((e >> 1) * 16 + (e & 1) * 2) * rows;
-    at<uint32_t>(q, off) = (hi[e] & 0xffffu) | (lo[e] << 16);
-    at<uint32_t>(q + rows, off) = (hi[e] >> 16) | (lo[e] & 0xffff0000u);
+    const int row = (e >> 1) * 16 + (e & 1) * 2;
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_amdgcn_perm(lo[e], hi[e], 0x05040100), b, off, row * words * 4, 0);          // low halves
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_amdgcn_perm(lo[e], hi[e], 0x07060302), b, off, (row + 1) * words * 4, 0);    // high halves
   }
 }
 
@@ -274,14 +282,60 @@ __device__ __forceinline__ f32x4 frag_mm(const uint16_t* a, const uint16_t* b, i
 
 // Workgroup n of `per` for each of `heads` heads -> (head, index): workgroups go to the eight XCDs (each with its own
 // L2) in turn, so a head's are given numbers of one XCD, which then reads the head's operands from HBM once
-__device__ __forceinline__ void xcd_head(int64_t n, int per, int64_t heads, int64_t& head, int& idx) {
+__device__ __forceinline__ void xcd_head(uint32_t n, uint32_t per, uint32_t heads, uint32_t& head, uint32_t& idx) {
   if (heads % 8 == 0) {
-    const int64_t m = n >> 3;
+    const uint32_t m = n >> 3;
     head = (m / per) * 8 + (n & 7);
-    idx = static_cast<int>(m % per);
+    idx = m % per;
   } else {
     head = n / per;
-    idx = static_cast<int>(n % per);
+    idx = n % per;
+  }
+}
+
+// A wave's 16 columns of a chunk's [64][d_v] rows as raw bits: elements of rows 16 mt + 4 g + e.  Rows behind the sequence
+// repeat its last one (what they hold meets zeros).  base: the chunk's first row of the head; row: bytes from token to
+// token; col: the lane's byte offset in a row
+template <class Raw>
+__device__ __forceinline__ void load_cols(uint32_t (&v)[4][4], const char* base, int row, int col, int64_t left, int g) {
+  const Buf b = buf_of(base);
+  auto ld = [&](int lane_off, int wave_off) -> uint32_t {
+    if constexpr (sizeof(Raw) == 2) return static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(b, lane_off, wave_off, 0));
+    else return __builtin_amdgcn_raw_buffer_load_b32(b, lane_off, wave_off, 0);
+  };
+  const int last = left < kC ? static_cast<int>(left) - 1 : kC - 1;   // one path for all chunks: no branch in the callers' loops
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = 16 * mt + 4 * g + e;
+      v[mt][e] = ld((t < last ? t : last) * row + col, 0);
+    }
+}
+
+// Its counterpart: rounds and stores the wave's columns
+template <Act A>
+__device__ __forceinline__ void store_cols(const f32x4 (&x)[4], char* base, int row, int col, int64_t left, int g, bool ok) {
+  const Buf b = buf_of(base);
+  auto st = [&](float v, int lane_off, int wave_off) {
+    if constexpr (A == Act::F32) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), b, lane_off, wave_off, 0);
+    else if constexpr (A == Act::BF16)
+      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v)), b, lane_off, wave_off, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<_Float16>(v)), b, lane_off, wave_off, 0);
+  };
+  if (!ok) return;
+  const int off = 4 * g * row + col;
+  if (left >= kC) {
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st(x[mt][e], off, (16 * mt + e) * row);
+  } else {
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (16 * mt + 4 * g + e < left) st(x[mt][e], off, (16 * mt + e) * row);
   }
 }
 

@@ -75,15 +75,14 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
   __shared__ __attribute__((aligned(16))) float s[4][kC];   // beta; beta e rk; exp(G_63 - G) rk; e rq
   const Dims& d = p.d;
   const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
-  int64_t bh;
-  int cb;
-  xcd_head(blockIdx.x, d.VP / 16, d.B * d.H, bh, cb);
-  const int64_t h = bh % d.H, b = bh / d.H, bg = b * d.G + h / (d.H / d.G);
+  uint32_t head, cb;
+  xcd_head(blockIdx.x, d.VP / 16, static_cast<uint32_t>(d.B * d.H), head, cb);
+  const uint32_t H = static_cast<uint32_t>(d.H), G = static_cast<uint32_t>(d.G);
+  const int64_t bh = head, h = head % H, b = head / H, bg = b * G + (head % H) / (H / G);
   const int col = cb * 16 + r;
   const bool ok = col < d.V;
-  const uint32_t vrow = static_cast<uint32_t>(d.H) * d.V * ES;
-  const uint32_t voff = vrow * 4 * g + (ok ? col : d.V - 1) * ES, yoff = vrow * 4 * g + col * ES;
-  const uint32_t poff = (4 * g * d.VP + col) * 4;
+  const int vrow = static_cast<int>(d.H) * d.V * ES, vcol = (ok ? col : d.V - 1) * ES;
+  const int poff = (4 * g * d.VP + col) * 4;
   const float so = p.so[bh], rso = 1.0f / so, rps = 1.0f / d.pscale, soc = ok ? so : 0.0f;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   f32x4 dS[MT];
@@ -92,22 +91,18 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
   h8 kf[NF], kt[NF], qt[NF], ph[6], pl[6], th[6], tl[6];
   float sc[4], el;
   uint32_t v[4][4];
-  auto frags = [&](h8* x, const uint16_t* base, int n) {
-#pragma unroll
-    for (int i = 0; i < n; ++i) x[i] = at<h8>(base + i * kFrag, lane * 16);
-  };
   auto KFp = [&](int64_t c) { return p.w.KF + (bg * d.nc + c) * (NP * NF * kFrag); };
   auto KTp = [&](int64_t c) { return p.w.KT + (bg * d.nc + c) * (NP * NF * kFrag); };
   auto QTp = [&](int64_t c) { return p.w.QT + (bg * d.nc + c) * (NP * NF * kFrag); };
   auto load_p = [&](int64_t c) {
     const uint16_t* x = p.w.PT + (bh * d.nc + c) * (12 * kFrag);
-    frags(ph, x, 6);
-    frags(pl, x + 6 * kFrag, 6);
+    load_frags(ph, x, lane);
+    load_frags(pl, x + 6 * kFrag, lane);
   };
   auto load_t = [&](int64_t c) {
     const uint16_t* x = p.w.TT + (bh * d.nc + c) * (12 * kFrag);
-    frags(th, x, 6);
-    frags(tl, x + 6 * kFrag, 6);
+    load_frags(th, x, lane);
+    load_frags(tl, x + 6 * kFrag, lane);
   };
   auto load_sc = [&](int64_t c) {
     const float* x = p.w.hsc + (bh * d.nc + c) * (kHeadSc * kC);
@@ -118,23 +113,14 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
     el = x[H_E * kC + kC - 1];
   };
   auto load_v = [&](int64_t c) {
-    const int64_t left = d.T - c * kC;
-    const char* base = static_cast<const char*>(p.dy) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES);
-    const int64_t row = fresh(vrow);
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[mt][e] = 0u;
-        if (left >= kC || 16 * mt + 4 * g + e < left) v[mt][e] = at<Raw>(base + (16 * mt + e) * row, voff);
-      }
+    load_cols<Raw>(v, static_cast<const char*>(p.dy) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES), vrow, vcol, d.T - c * kC, g);
   };
   if (AHEAD) {
-    frags(kf, KFp(d.nc - 1), NF);
+    load_frags(kf, KFp(d.nc - 1), lane);
     load_p(d.nc - 1);
     load_t(d.nc - 1);
-    frags(kt, KTp(d.nc - 1), NF);
-    frags(qt, QTp(d.nc - 1), NF);
+    load_frags(kt, KTp(d.nc - 1), lane);
+    load_frags(qt, QTp(d.nc - 1), lane);
   }
   load_sc(d.nc - 1);
   load_v(d.nc - 1);
@@ -148,7 +134,7 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
     const float elc = el;
     if (c > 0) load_sc(c - 1);
     if (!AHEAD) {
-      frags(kf, KFp(c), NF);
+      load_frags(kf, KFp(c), lane);
       load_p(c);
     }
     f32x4 dU[4] = {zero, zero, zero, zero}, pd[4] = {zero, zero, zero, zero}, dO[4];
@@ -165,7 +151,7 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
         for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(at<h8>(KFp(c) + (NF + mt * KS + ks) * kFrag, lane * 16), f.hi, dU[mt]);
       }
     }
-    if (more) frags(kf, KFp(c - 1), NF);
+    if (more) load_frags(kf, KFp(c - 1), lane);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -183,8 +169,8 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
     if (more) load_p(c - 1);
     if (!AHEAD) {
       load_t(c);
-      frags(kt, KTp(c), NF);
-      frags(qt, QTp(c), NF);
+      load_frags(kt, KTp(c), lane);
+      load_frags(qt, QTp(c), lane);
     }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
@@ -225,25 +211,16 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
         dS[mt] = mma(at<h8>(QTp(c) + (NF + 2 * mt + 1) * kFrag, lane * 16), e1.hi, dS[mt]);
       }
     }
-    if (more) frags(qt, QTp(c - 1), NF);
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) Y[mt][e] *= 1.0f / kTScale;
+    if (more) load_frags(qt, QTp(c - 1), lane);
     store_packed(p.DU + ci * kC * d.VP, poff, to_b(Y[0], Y[1]), d.VP);
     store_packed(p.DU + (ci * kC + 32) * d.VP, poff, to_b(Y[2], Y[3]), d.VP);
-    char* out = static_cast<char*>(p.d_v) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES);
-    const int64_t yrow = fresh(vrow);
+    f32x4 dv[4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      const f32x4 be = *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * g), bk = *reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * g);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (ok && (left >= kC || 16 * mt + 4 * g + e < left))
-          IO<A>::st(&at<char>(out + (16 * mt + e) * yrow, yoff), 0, be[e] * Y[mt][e] * rso);
-        Y[mt][e] *= -bk[e];
-      }
+      dv[mt] = Y[mt] * *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * g) * rso;
+      Y[mt] *= -*reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * g);
     }
+    store_cols<A>(dv, static_cast<char*>(p.d_v) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES), vrow, col * ES, left, g, ok);
     const Frag y0 = to_b(Y[0], Y[1]), y1 = to_b(Y[2], Y[3]);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(kt[2 * mt], y0.hi, dS[mt]);
@@ -260,7 +237,7 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
         dS[mt] = mma(at<h8>(KTp(c) + (NF + 2 * mt + 1) * kFrag, lane * 16), y1.hi, dS[mt]);
       }
     }
-    if (more) frags(kt, KTp(c - 1), NF);
+    if (more) load_frags(kt, KTp(c - 1), lane);
   }
 }
 

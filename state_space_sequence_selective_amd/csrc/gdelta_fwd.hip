@@ -36,7 +36,9 @@ __global__ void __launch_bounds__(256) gdelta_rows_kernel(const FwdArgs p) {
     for (int e = 0; e < EPT; ++e) m = max_finite(m, x[which][e]);
     m = fmaxf(m, __shfl_xor(m, 1, 64));
     m = fmaxf(m, __shfl_xor(m, 2, 64));
-    const float pw = pow2_below(m, 2);
+    // a row of zeros (those behind the sequence too) takes a power of two that keeps its scale, 1 / (sqrt(eps) pw), near 1:
+    // what it multiplies has to stay inside f16 although it then meets zeros
+    const float pw = m > 0.0f ? pow2_below(m, 2) : pow2_below(sqrtf(d.eps), 1);
 #pragma unroll
     for (int e = 0; e < EPT; ++e) {
       x[which][e] *= pw;
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
         v[o] = tr ? (x >= i ? sT[x * kAS + i] : 0.0f) : (x <= i ? sT[i * kAS + x] : 0.0f);
       }
       uint32_t a, bb;
-      split2(v[0] * kTScale, v[1] * kTScale, a, bb);
+      split2(v[0], v[1], a, bb);
       hi[e] = a;
       lo[e] = bb;
     }
@@ -311,147 +313,122 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
 }
 
 // ------------------------------------------------------------------ pass over the chunks
-// A wave holds 16 columns of one head's S^T (rows: d_k) in registers, as the accumulators of the state update; they
-// are at once the B operand of the products with k and q, and u is one for the update, so a wave needs nothing of any
-// other: no LDS but for its tokens' scalars, no barrier.  The next chunk's fragments are loaded as soon as this one's
-// are used.
-template <Act A, int KP, bool SAVE>
-__global__ void __launch_bounds__(64) gdelta_fwd_kernel(const FwdArgs p) {
-  constexpr int NP = A == Act::F32 ? 2 : 1, MT = KP / 16, KS = KP / 32, NF = KP / 8, PP = kPPlanes<A>;
-  constexpr bool AHEAD = NP == 1;   // two planes do not fit the registers: loaded where they are used
-  using Raw = std::conditional_t<A == Act::F32, uint32_t, uint16_t>;
-  constexpr int ES = sizeof(Raw);
-  __shared__ __attribute__((aligned(16))) float s[4][kC];   // beta; beta e rk; exp(G_63 - G) rk; e rq
-  const Dims& d = p.d;
-  const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
-  int64_t bh;
-  int cb;
-  xcd_head(blockIdx.x, d.VP / 16, d.B * d.H, bh, cb);
-  const int64_t h = bh % d.H, b = bh / d.H, hk = h / (d.H / d.G), bg = b * d.G + hk;
-  const int col = cb * 16 + r;
-  const bool ok = col < d.V;
-  const uint32_t vrow = static_cast<uint32_t>(d.H) * d.V * ES;   // bytes of a token's v
-  const uint32_t voff = vrow * 4 * g + (ok ? col : d.V - 1) * ES, yoff = vrow * 4 * g + col * ES;
-  const uint32_t poff = (4 * g * d.VP + col) * 4;                // this lane's place in the packed S and U
-  // the head's power of two: |s|, |v - S k| <= 2 sqrt(T + 1) max(|v|, |h0|) scaled below 2^15
-  float m = 0.0f;
-  for (int64_t i = lane; i < d.nc; i += 64) m = fmaxf(m, p.w.vmax[bh * d.nc + i]);
-  const float sv = pow2_below(wave_max(m), 15 - static_cast<int>(ceilf(1.0f + 0.5f * log2f(static_cast<float>(d.T) + 1.0f))));
-  const float rsv = 1.0f / sv, rps = 1.0f / d.pscale, svc = ok ? sv : 0.0f;
-  if (SAVE && lane == 0 && cb == 0) p.w.sv[bh] = sv;
+// 16 columns of one head's S^T (rows: d_k) to a wave, or to two.  The chain from chunk to chunk (k S, T x, k^T u: 82
+// matrix instructions of 16 cycles for d_k = 128) holds the state in registers, as the accumulators of its update; they
+// are at once the B operand of its product with k, and u is one for the update, so it needs nothing of other lanes.  The
+// output (y, and what a backward pass reads) takes the parts of S and u: of the same wave, or of the first wave through
+// LDS, a chunk behind.  Two waves halve the chain's time a chunk where there are SIMDs for both.  Every family of
+// fragments is loaded a chunk ahead, as soon as this chunk's are used; the last chunk loads its own again, so that the
+// loop has no branch.
+template <int KP>
+struct PassBuf {
+  h8 S[KP / 32][2][64], U[2][2][64];   // [step][high, low][lane]
+};
 
-  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+template <Act A>
+struct PassPlace {   // where a wave's columns are
+  using Raw = std::conditional_t<A == Act::F32, uint32_t, uint16_t>;
+  static constexpr int ES = sizeof(Raw);
+  int lane, r, g, col, row;   // row: bytes from token to token
+  bool ok;
+  int64_t bh, h, b, bg, nc, T, HV;
+
+  __device__ __forceinline__ explicit PassPlace(const Dims& d) {
+    lane = threadIdx.x & 63;
+    r = lane & 15;
+    g = lane >> 4;
+    uint32_t head, cb;
+    xcd_head(blockIdx.x, d.VP / 16, static_cast<uint32_t>(d.B * d.H), head, cb);
+    const uint32_t H = static_cast<uint32_t>(d.H), G = static_cast<uint32_t>(d.G);
+    bh = head;
+    h = head % H;
+    b = head / H;
+    bg = b * G + (head % H) / (H / G);
+    col = cb * 16 + r;
+    ok = col < d.V;
+    row = static_cast<int>(d.H) * d.V * ES;
+    nc = d.nc;
+    T = d.T;
+    HV = h * d.V * ES;
+  }
+  __device__ __forceinline__ int64_t at_chunk(int64_t c) const { return (b * T + c * kC) * row + HV; }
+};
+
+template <Act A, int KP>
+struct Chain {
+  static constexpr int NP = A == Act::F32 ? 2 : 1, MT = KP / 16, KS = KP / 32, NF = KP / 8;
+  using Place = PassPlace<A>;
   f32x4 S[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    S[mt] = zero;
-    const int row = 16 * mt + 4 * g;
-    if (p.h0 && ok && row < d.K) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(p.h0 + (bh * d.V + col) * d.K + row);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[mt][e] = x[e] * sv;
-    }
-  }
-  h8 kf[NF], qf[NF], kt[NF], pf[6], th[6], tl[6];
-  float sc[4], el;
+  h8 kf[NF], kt[NF], th[6], tl[6];
+  float sc[3], el;
   uint32_t v[4][4];
-  auto frags = [&](h8* x, const uint16_t* base, int n) {
-#pragma unroll
-    for (int i = 0; i < n; ++i) x[i] = at<h8>(base + i * kFrag, lane * 16);
-  };
-  auto KFp = [&](int64_t c) { return p.w.KF + (bg * d.nc + c) * (NP * NF * kFrag); };
-  auto QFp = [&](int64_t c) { return p.w.QF + (bg * d.nc + c) * (NP * NF * kFrag); };
-  auto KTp = [&](int64_t c) { return p.w.KT + (bg * d.nc + c) * (NP * NF * kFrag); };
-  auto Pp = [&](int64_t c) { return p.w.P + (bh * d.nc + c) * (PP * 6 * kFrag); };
-  auto Tp = [&](int64_t c) { return p.w.T + (bh * d.nc + c) * (12 * kFrag); };
-  auto load_t = [&](int64_t c) {
-    frags(th, Tp(c), 6);
-    frags(tl, Tp(c) + 6 * kFrag, 6);
-  };
-  auto load_sc = [&](int64_t c) {
-    const float* x = p.w.hsc + (bh * d.nc + c) * (kHeadSc * kC);
-    sc[0] = x[H_BETA * kC + lane];
-    sc[1] = x[H_BK * kC + lane];
-    sc[2] = x[H_DK * kC + lane];
-    sc[3] = x[H_EQ * kC + lane];
-    el = x[H_E * kC + kC - 1];
-  };
-  auto load_v = [&](int64_t c) {
-    const int64_t left = d.T - c * kC;
-    const char* base = static_cast<const char*>(p.v) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES);
-    const int64_t row = fresh(vrow);
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[mt][e] = 0u;
-        if (left >= kC || 16 * mt + 4 * g + e < left) v[mt][e] = at<Raw>(base + (16 * mt + e) * row, voff);
-      }
-  };
-  if (AHEAD) {
-    frags(kf, KFp(0), NF);
-    frags(qf, QFp(0), NF);
-    load_t(0);
-    frags(kt, KTp(0), NF);
-    frags(pf, Pp(0), 6);
+
+  __device__ __forceinline__ const uint16_t* KF(const FwdArgs& p, const Place& w, int64_t c) const { return p.w.KF + (w.bg * w.nc + c) * (NP * NF * kFrag); }
+  __device__ __forceinline__ const uint16_t* KT(const FwdArgs& p, const Place& w, int64_t c) const { return p.w.KT + (w.bg * w.nc + c) * (NP * NF * kFrag); }
+  __device__ __forceinline__ void load_t(const FwdArgs& p, const Place& w, int64_t c) {
+    const uint16_t* x = p.w.T + (w.bh * w.nc + c) * (12 * kFrag);
+    load_frags(th, x, w.lane);
+    load_frags(tl, x + 6 * kFrag, w.lane);
   }
-  load_sc(0);
-  load_v(0);
-  for (int64_t c = 0; c < d.nc; ++c) {
-    const int64_t left = d.T - c * kC, ci = bh * d.nc + c;
-    const bool more = AHEAD && c + 1 < d.nc;
+  __device__ __forceinline__ void load_sc(const FwdArgs& p, const Place& w, int64_t c, float sv) {
+    const float* x = p.w.hsc + (w.bh * w.nc + c) * (kHeadSc * kC);
+    sc[0] = x[H_BETA * kC + w.lane] * sv;
+    sc[1] = x[H_BK * kC + w.lane];
+    sc[2] = x[H_DK * kC + w.lane];
+    el = x[H_E * kC + kC - 1];
+  }
+  __device__ __forceinline__ void load_v(const FwdArgs& p, const Place& w, int64_t c) {
+    // columns behind d_v repeat the last one: whatever they hold meets zeros in the backward pass
+    const int vcol = w.ok ? w.col : static_cast<int>(p.d.V) - 1;
+    load_cols<typename Place::Raw>(v, static_cast<const char*>(p.v) + w.at_chunk(c), w.row, vcol * Place::ES, w.T - c * kC, w.g);
+  }
+  __device__ __forceinline__ void init(const FwdArgs& p, const Place& w, float sv) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      S[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      const int row = 16 * mt + 4 * w.g;
+      if (p.h0 && w.ok && row < p.d.K) S[mt] = *reinterpret_cast<const f32x4*>(p.h0 + (w.bh * p.d.V + w.col) * p.d.K + row) * sv;
+    }
+    load_frags(kf, KF(p, w, 0), w.lane);
+    load_sc(p, w, 0, sv);
+    load_t(p, w, 0);
+    load_v(p, w, 0);
+    load_frags(kt, KT(p, w, 0), w.lane);
+  }
+  // One chunk.  on_state(step, parts) for the entering state, on_u(parts, parts) for u.  s: [3][64] floats of the wave.
+  template <class OnState, class OnU>
+  __device__ __forceinline__ void step(const FwdArgs& p, const Place& w, int64_t c, float sv, float (*s)[kC], OnState on_state, OnU on_u) {
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t next = c + 1 < w.nc ? c + 1 : c;
     mscan::wave_lds_sync();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i][lane] = sc[i];
+    for (int i = 0; i < 3; ++i) s[i][w.lane] = sc[i];
     mscan::wave_lds_sync();
     const float elc = el;
-    if (c + 1 < d.nc) load_sc(c + 1);
-    if (!AHEAD) {
-      frags(kf, KFp(c), NF);
-      frags(qf, QFp(c), NF);
-    }
-    f32x4 ak[4], aq[4];
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) ak[mt] = aq[mt] = zero;
+    load_sc(p, w, next, sv);
+    f32x4 x[4] = {zero, zero, zero, zero};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const Frag f = to_b(S[2 * ks], S[2 * ks + 1]);
-      if (SAVE) store_packed(p.w.S + (ci * KP + 32 * ks) * d.VP, poff, f, d.VP);
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) ak[mt] = mma(kf[mt * KS + ks], f.hi, ak[mt]);
+      for (int mt = 0; mt < 4; ++mt) x[mt] = mma(kf[mt * KS + ks], f.hi, x[mt]);
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) ak[mt] = mma(kf[mt * KS + ks], f.lo, ak[mt]);
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) aq[mt] = mma(qf[mt * KS + ks], f.hi, aq[mt]);
-      if (PP == 2) {
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) aq[mt] = mma(qf[mt * KS + ks], f.lo, aq[mt]);
-      }
+      for (int mt = 0; mt < 4; ++mt) x[mt] = mma(kf[mt * KS + ks], f.lo, x[mt]);
       if (NP == 2) {
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-          ak[mt] = mma(at<h8>(KFp(c) + (NF + mt * KS + ks) * kFrag, lane * 16), f.hi, ak[mt]);
-          aq[mt] = mma(at<h8>(QFp(c) + (NF + mt * KS + ks) * kFrag, lane * 16), f.hi, aq[mt]);
-        }
+        for (int mt = 0; mt < 4; ++mt) x[mt] = mma(at<h8>(KF(p, w, c) + (NF + mt * KS + ks) * kFrag, w.lane * 16), f.hi, x[mt]);
       }
+      on_state(ks, f);
     }
-    if (more) {
-      frags(kf, KFp(c + 1), NF);
-      frags(qf, QFp(c + 1), NF);
-    }
+    load_frags(kf, KF(p, w, next), w.lane);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      const f32x4 be = *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * g), bk = *reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * g);
+      const f32x4 be = *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * w.g), bk = *reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * w.g);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ak[mt][e] = fmaf(be[e], IO<A>::cvt(v[mt][e]) * svc, -bk[e] * ak[mt][e]);
+      for (int e = 0; e < 4; ++e) x[mt][e] = fmaf(be[e], IO<A>::cvt(v[mt][e]), -bk[e] * x[mt][e]);
     }
-    if (c + 1 < d.nc) load_v(c + 1);
-    if (!AHEAD) {
-      load_t(c);
-      frags(kt, KTp(c), NF);
-      frags(pf, Pp(c), 6);
-    }
-    const Frag x0 = to_b(ak[0], ak[1]), x1 = to_b(ak[2], ak[3]);
+    load_v(p, w, next);
+    const Frag x0 = to_b(x[0], x[1]), x1 = to_b(x[2], x[3]);
     f32x4 U[4] = {zero, zero, zero, zero};
 #pragma unroll
     for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(th[f], (kLk[f] ? x1 : x0).hi, U[kLm[f]]);
@@ -459,22 +436,13 @@ __global__ void __launch_bounds__(64) gdelta_fwd_kernel(const FwdArgs p) {
     for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(th[f], (kLk[f] ? x1 : x0).lo, U[kLm[f]]);
 #pragma unroll
     for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(tl[f], (kLk[f] ? x1 : x0).hi, U[kLm[f]]);
-    if (more) load_t(c + 1);
+    load_t(p, w, next);
     f32x4 D[4];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      const f32x4 dk = *reinterpret_cast<const f32x4*>(s[2] + 16 * mt + 4 * g);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        U[mt][e] *= 1.0f / kTScale;
-        D[mt][e] = U[mt][e] * dk[e];
-      }
-    }
+    for (int mt = 0; mt < 4; ++mt) D[mt] = U[mt] * *reinterpret_cast<const f32x4*>(s[2] + 16 * mt + 4 * w.g);
     const Frag d0 = to_b(D[0], D[1]), d1 = to_b(D[2], D[3]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[mt][e] *= elc;
+    for (int mt = 0; mt < MT; ++mt) S[mt] *= elc;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) S[mt] = mma(kt[2 * mt], d0.hi, S[mt]);
 #pragma unroll
@@ -486,49 +454,157 @@ __global__ void __launch_bounds__(64) gdelta_fwd_kernel(const FwdArgs p) {
     if (NP == 2) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        S[mt] = mma(at<h8>(KTp(c) + (NF + 2 * mt) * kFrag, lane * 16), d0.hi, S[mt]);
-        S[mt] = mma(at<h8>(KTp(c) + (NF + 2 * mt + 1) * kFrag, lane * 16), d1.hi, S[mt]);
+        S[mt] = mma(at<h8>(KT(p, w, c) + (NF + 2 * mt) * kFrag, w.lane * 16), d0.hi, S[mt]);
+        S[mt] = mma(at<h8>(KT(p, w, c) + (NF + 2 * mt + 1) * kFrag, w.lane * 16), d1.hi, S[mt]);
       }
     }
-    if (more) frags(kt, KTp(c + 1), NF);
-    const Frag u0 = to_b(U[0], U[1]), u1 = to_b(U[2], U[3]);
-    if (SAVE) {
-      store_packed(p.w.U + ci * kC * d.VP, poff, u0, d.VP);
-      store_packed(p.w.U + (ci * kC + 32) * d.VP, poff, u1, d.VP);
+    load_frags(kt, KT(p, w, next), w.lane);
+    on_u(to_b(U[0], U[1]), to_b(U[2], U[3]));
+  }
+  __device__ __forceinline__ void finish(const FwdArgs& p, const Place& w, float rsv) const {
+    if (!p.h_last || !w.ok) return;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int row = 16 * mt + 4 * w.g;
+      if (row < p.d.K) *reinterpret_cast<f32x4*>(p.h_last + (w.bh * p.d.V + w.col) * p.d.K + row) = S[mt] * rsv;
     }
-    f32x4 y[4] = {zero, zero, zero, zero};
+  }
+};
+
+template <Act A, int KP, bool SAVE>
+struct Output {
+  static constexpr int NP = A == Act::F32 ? 2 : 1, KS = KP / 32, NF = KP / 8, PP = kPPlanes<A>;
+  using Place = PassPlace<A>;
+  h8 qf[NF], pf[6];
+  float eq;
+  f32x4 y[4];
+
+  __device__ __forceinline__ const uint16_t* QF(const FwdArgs& p, const Place& w, int64_t c) const { return p.w.QF + (w.bg * w.nc + c) * (NP * NF * kFrag); }
+  __device__ __forceinline__ const uint16_t* P(const FwdArgs& p, const Place& w, int64_t c) const { return p.w.P + (w.bh * w.nc + c) * (PP * 6 * kFrag); }
+  __device__ __forceinline__ void load_q(const FwdArgs& p, const Place& w, int64_t c) {
+    load_frags(qf, QF(p, w, c), w.lane);
+    eq = p.w.hsc[(w.bh * w.nc + c) * (kHeadSc * kC) + H_EQ * kC + w.lane] * p.d.pscale;
+  }
+  __device__ __forceinline__ void load_p(const FwdArgs& p, const Place& w, int64_t c) { load_frags(pf, P(p, w, c), w.lane); }
+  __device__ __forceinline__ void begin(const Place& w, float* s) {
+    mscan::wave_lds_sync();
+    s[w.lane] = eq;
+    mscan::wave_lds_sync();
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) y[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  __device__ __forceinline__ void state(const FwdArgs& p, const Place& w, int64_t c, int ks, const Frag& f) {
+    if (SAVE) store_packed(p.w.S + ((w.bh * w.nc + c) * KP + 32 * ks) * p.d.VP, (4 * w.g * p.d.VP + w.col) * 4, f, p.d.VP);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) y[mt] = mma(qf[mt * KS + ks], f.hi, y[mt]);
+    if (PP == 2) {
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) y[mt] = mma(qf[mt * KS + ks], f.lo, y[mt]);
+    }
+    if (NP == 2) {
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) y[mt] = mma(at<h8>(QF(p, w, c) + (NF + mt * KS + ks) * kFrag, w.lane * 16), f.hi, y[mt]);
+    }
+  }
+  __device__ __forceinline__ void u(const FwdArgs& p, const Place& w, int64_t c, float scale, const float* s, const Frag& u0, const Frag& u1) {
+    const int64_t ci = w.bh * w.nc + c, next = c + 1 < w.nc ? c + 1 : c;
+    load_q(p, w, next);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) y[mt] *= *reinterpret_cast<const f32x4*>(s + 16 * mt + 4 * w.g);
+    if (SAVE) {
+      const int off = (4 * w.g * p.d.VP + w.col) * 4;
+      store_packed(p.w.U + ci * kC * p.d.VP, off, u0, p.d.VP);
+      store_packed(p.w.U + (ci * kC + 32) * p.d.VP, off, u1, p.d.VP);
+    }
 #pragma unroll
     for (int f = 0; f < 6; ++f) y[kLm[f]] = mma(pf[f], (kLk[f] ? u1 : u0).hi, y[kLm[f]]);
     if (PP == 2) {
 #pragma unroll
       for (int f = 0; f < 6; ++f) {
         y[kLm[f]] = mma(pf[f], (kLk[f] ? u1 : u0).lo, y[kLm[f]]);
-        y[kLm[f]] = mma(at<h8>(Pp(c) + (6 + f) * kFrag, lane * 16), (kLk[f] ? u1 : u0).hi, y[kLm[f]]);
+        y[kLm[f]] = mma(at<h8>(P(p, w, c) + (6 + f) * kFrag, w.lane * 16), (kLk[f] ? u1 : u0).hi, y[kLm[f]]);
       }
     }
-    if (more) frags(pf, Pp(c + 1), 6);
-    char* out = static_cast<char*>(p.y) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES);
-    const int64_t yrow = fresh(vrow);
+    load_p(p, w, next);
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      const f32x4 eq = *reinterpret_cast<const f32x4*>(s[3] + 16 * mt + 4 * g);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (ok && (left >= kC || 16 * mt + 4 * g + e < left))
-          IO<A>::st(&at<char>(out + (16 * mt + e) * yrow, yoff), 0, fmaf(eq[e], aq[mt][e], y[mt][e] * rps) * rsv);
-    }
+    for (int mt = 0; mt < 4; ++mt) y[mt] *= scale;
+    store_cols<A>(y, static_cast<char*>(p.y) + w.at_chunk(c), w.row, w.col * Place::ES, w.T - c * kC, w.g, w.ok);
   }
-  if (p.h_last && ok) {
+};
+
+template <Act A, int KP, bool SAVE, bool PAIR>
+__global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdArgs p) {
+  constexpr int KS = KP / 32;
+  constexpr bool LOW = SAVE || kPPlanes<A> == 2;   // the output takes the low parts too
+  __shared__ __attribute__((aligned(16))) float s[4][kC];   // beta sv; beta e rk; exp(G_63 - G) rk / e rq pscale
+  const Dims& d = p.d;
+  const PassPlace<A> w(d);
+  // the head's power of two: |s|, |v - S k| <= 2 sqrt(T + 1) max(|v|, |h0|) scaled below 2^15
+  float m = 0.0f;
+  for (int64_t i = w.lane; i < d.nc; i += 64) m = fmaxf(m, p.w.vmax[w.bh * d.nc + i]);
+  const float sv = pow2_below(wave_max(m), 15 - static_cast<int>(ceilf(1.0f + 0.5f * log2f(static_cast<float>(d.T) + 1.0f))));
+  const float rsv = 1.0f / sv, yscale = rsv / d.pscale;
+  if (SAVE && threadIdx.x == 0 && w.col < 16) p.w.sv[w.bh] = sv;
+  if constexpr (PAIR) {
+    __shared__ __attribute__((aligned(16))) PassBuf<KP> buf[2];
+    if (wave_id() == 0) {
+      Chain<A, KP> ch;
+      ch.init(p, w, sv);
+      for (int64_t c = 0; c < d.nc; ++c) {
+        PassBuf<KP>& o = buf[c & 1];
+        ch.step(p, w, c, sv, s,
+                [&](int ks, const Frag& f) {
+                  o.S[ks][0][w.lane] = f.hi;
+                  if (LOW) o.S[ks][1][w.lane] = f.lo;
+                },
+                [&](const Frag& u0, const Frag& u1) {
+                  o.U[0][0][w.lane] = u0.hi;
+                  o.U[1][0][w.lane] = u1.hi;
+                  if (LOW) {
+                    o.U[0][1][w.lane] = u0.lo;
+                    o.U[1][1][w.lane] = u1.lo;
+                  }
+                });
+        mscan::lds_barrier();   // chunk c's parts are there, and the other wave is done with those of chunk c - 1
+      }
+      ch.finish(p, w, rsv);
+    } else {
+      Output<A, KP, SAVE> out;
+      out.load_q(p, w, 0);
+      out.load_p(p, w, 0);
+      for (int64_t c = 0; c < d.nc; ++c) {
+        const PassBuf<KP>& o = buf[c & 1];
+        out.begin(w, s[3]);
+        mscan::lds_barrier();
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int row = 16 * mt + 4 * g;
-      if (row < d.K) {
-        f32x4 x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = S[mt][e] * rsv;
-        *reinterpret_cast<f32x4*>(p.h_last + (bh * d.V + col) * d.K + row) = x;
+        for (int ks = 0; ks < KS; ++ks) {
+          Frag f;
+          f.hi = o.S[ks][0][w.lane];
+          if (LOW) f.lo = o.S[ks][1][w.lane];
+          out.state(p, w, c, ks, f);
+        }
+        Frag u0, u1;
+        u0.hi = o.U[0][0][w.lane];
+        u1.hi = o.U[1][0][w.lane];
+        if (LOW) {
+          u0.lo = o.U[0][1][w.lane];
+          u1.lo = o.U[1][1][w.lane];
+        }
+        out.u(p, w, c, yscale, s[3], u0, u1);
       }
     }
+  } else {
+    Chain<A, KP> ch;
+    Output<A, KP, SAVE> out;
+    ch.init(p, w, sv);
+    out.load_q(p, w, 0);
+    out.load_p(p, w, 0);
+    for (int64_t c = 0; c < d.nc; ++c) {
+      out.begin(w, s[3]);
+      ch.step(p, w, c, sv, s, [&](int ks, const Frag& f) { out.state(p, w, c, ks, f); },
+              [&](const Frag& u0, const Frag& u1) { out.u(p, w, c, yscale, s[3], u0, u1); });
+    }
+    ch.finish(p, w, rsv);
   }
 }
 
@@ -662,9 +738,14 @@ hipError_t launch_chunks(const FwdArgs& a, bool save, hipStream_t st) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((gdelta_prep_kernel<A, KP>), dim3(bh * nc), dim3(256), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const dim3 grid(bh * (d.VP / 16));
-  if (save) hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, true>), grid, dim3(64), 0, st, a);
-  else hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, false>), grid, dim3(64), 0, st, a);
+  const unsigned tiles = bh * (d.VP / 16);
+  if (tiles <= kPairTiles) {
+    if (save) hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, true, true>), dim3(tiles), dim3(128), 0, st, a);
+    else hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, false, true>), dim3(tiles), dim3(128), 0, st, a);
+  } else {
+    if (save) hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, true, false>), dim3(tiles), dim3(64), 0, st, a);
+    else hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, false, false>), dim3(tiles), dim3(64), 0, st, a);
+  }
   return hipGetLastError();
 }
 
