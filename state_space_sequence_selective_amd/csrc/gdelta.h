@@ -179,6 +179,23 @@ __device__ __forceinline__ void load_frags(h8 (&x)[N], const void* base, int lan
   for (int i = 0; i < N; ++i) x[i] = buf_h8(b, lane * 16 + (i & 3) * 1024, (i >> 2) * 4096);
 }
 
+// Copies fragments `first`, first + STEP, .. of N from global memory into LDS, asynchronously and without registers
+// (global_load_lds: 16 bytes a lane to consecutive places); wait_copies() ends it
+template <int N, int STEP>
+__device__ __forceinline__ void copy_frags(uint16_t* dst, const uint16_t* src, int first, int lane) {
+#pragma unroll
+  for (int i = 0; i < (N + STEP - 1) / STEP; ++i) {
+    const int f = first + i * STEP;
+    if (N % STEP == 0 || f < N)
+      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)(const_cast<uint16_t*>(src) + f * kFrag + lane * 8),
+                                       (__attribute__((address_space(3))) void*)(dst + f * kFrag), 16, 0, 0);
+  }
+}
+__device__ __forceinline__ void wait_copies() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_s_waitcnt(0);
+}
+
 // Stores a split operand's parts as f16 high | low << 16 words to its 4 + 4 rows 4 g + e, 16 + 4 g + e of `words` words;
 // off: the lane's byte offset in the first of them
 __device__ __forceinline__ void store_packed(uint32_t* base, int off, const Frag& f, int words) {

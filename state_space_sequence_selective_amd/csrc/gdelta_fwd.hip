@@ -333,18 +333,19 @@ struct PassPlace {   // where a wave's columns are
   bool ok;
   int64_t bh, h, b, bg, nc, T, HV;
 
-  __device__ __forceinline__ explicit PassPlace(const Dims& d) {
+  // `tiles` 16-column tiles to a workgroup, of which this wave has number `tile`
+  __device__ __forceinline__ explicit PassPlace(const Dims& d, int tiles = 1, int tile = 0) {
     lane = threadIdx.x & 63;
     r = lane & 15;
     g = lane >> 4;
     uint32_t head, cb;
-    xcd_head(blockIdx.x, d.VP / 16, static_cast<uint32_t>(d.B * d.H), head, cb);
+    xcd_head(blockIdx.x, (d.VP / 16 + tiles - 1) / tiles, static_cast<uint32_t>(d.B * d.H), head, cb);
     const uint32_t H = static_cast<uint32_t>(d.H), G = static_cast<uint32_t>(d.G);
     bh = head;
     h = head % H;
     b = head / H;
     bg = b * G + (head % H) / (H / G);
-    col = cb * 16 + r;
+    col = (cb * tiles + tile) * 16 + r;
     ok = col < d.V;
     row = static_cast<int>(d.H) * d.V * ES;
     nc = d.nc;
@@ -354,21 +355,39 @@ struct PassPlace {   // where a wave's columns are
   __device__ __forceinline__ int64_t at_chunk(int64_t c) const { return (b * T + c * kC) * row + HV; }
 };
 
+// Fragments of a chunk in a shared buffer, in this order; 16-bit inputs only
 template <Act A, int KP>
+struct FwdRing {
+  static constexpr int NF = KP / 8, KF = 0, QF = NF, T = 2 * NF, KT = T + 12, P = KT + NF, N = P + 6 * kPPlanes<A>;
+};
+
+// RING: fragments come from the shared buffer instead of registers
+template <Act A, int KP, bool RING>
 struct Chain {
   static constexpr int NP = A == Act::F32 ? 2 : 1, MT = KP / 16, KS = KP / 32, NF = KP / 8;
   using Place = PassPlace<A>;
+  using R = FwdRing<A, KP>;
   f32x4 S[MT];
-  h8 kf[NF], kt[NF], th[6], tl[6];
+  h8 kf[RING ? 1 : NF], kt[RING ? 1 : NF], th[RING ? 1 : 6], tl[RING ? 1 : 6];
   float sc[3], el;
   uint32_t v[4][4];
+  const uint16_t* ring;   // + this lane's place
 
+  template <int N>
+  __device__ __forceinline__ h8 get(const h8 (&x)[N], int base, int i) const {
+    if constexpr (RING) return ld8(ring + (base + i) * kFrag);
+    else return x[i];
+  }
+  template <int N>
+  __device__ __forceinline__ void load(h8 (&x)[N], const uint16_t* base, int lane) {
+    if constexpr (!RING) load_frags(x, base, lane);
+  }
   __device__ __forceinline__ const uint16_t* KF(const FwdArgs& p, const Place& w, int64_t c) const { return p.w.KF + (w.bg * w.nc + c) * (NP * NF * kFrag); }
   __device__ __forceinline__ const uint16_t* KT(const FwdArgs& p, const Place& w, int64_t c) const { return p.w.KT + (w.bg * w.nc + c) * (NP * NF * kFrag); }
   __device__ __forceinline__ void load_t(const FwdArgs& p, const Place& w, int64_t c) {
     const uint16_t* x = p.w.T + (w.bh * w.nc + c) * (12 * kFrag);
-    load_frags(th, x, w.lane);
-    load_frags(tl, x + 6 * kFrag, w.lane);
+    load(th, x, w.lane);
+    load(tl, x + 6 * kFrag, w.lane);
   }
   __device__ __forceinline__ void load_sc(const FwdArgs& p, const Place& w, int64_t c, float sv) {
     const float* x = p.w.hsc + (w.bh * w.nc + c) * (kHeadSc * kC);
@@ -389,11 +408,11 @@ struct Chain {
       const int row = 16 * mt + 4 * w.g;
       if (p.h0 && w.ok && row < p.d.K) S[mt] = *reinterpret_cast<const f32x4*>(p.h0 + (w.bh * p.d.V + w.col) * p.d.K + row) * sv;
     }
-    load_frags(kf, KF(p, w, 0), w.lane);
+    load(kf, KF(p, w, 0), w.lane);
     load_sc(p, w, 0, sv);
     load_t(p, w, 0);
     load_v(p, w, 0);
-    load_frags(kt, KT(p, w, 0), w.lane);
+    load(kt, KT(p, w, 0), w.lane);
   }
   // One chunk.  on_state(step, parts) for the entering state, on_u(parts, parts) for u.  s: [3][64] floats of the wave.
   template <class OnState, class OnU>
@@ -411,16 +430,16 @@ struct Chain {
     for (int ks = 0; ks < KS; ++ks) {
       const Frag f = to_b(S[2 * ks], S[2 * ks + 1]);
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) x[mt] = mma(kf[mt * KS + ks], f.hi, x[mt]);
+      for (int mt = 0; mt < 4; ++mt) x[mt] = mma(get(kf, R::KF, mt * KS + ks), f.hi, x[mt]);
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) x[mt] = mma(kf[mt * KS + ks], f.lo, x[mt]);
+      for (int mt = 0; mt < 4; ++mt) x[mt] = mma(get(kf, R::KF, mt * KS + ks), f.lo, x[mt]);
       if (NP == 2) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) x[mt] = mma(at<h8>(KF(p, w, c) + (NF + mt * KS + ks) * kFrag, w.lane * 16), f.hi, x[mt]);
       }
       on_state(ks, f);
     }
-    load_frags(kf, KF(p, w, next), w.lane);
+    load(kf, KF(p, w, next), w.lane);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
       const f32x4 be = *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * w.g), bk = *reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * w.g);
@@ -431,11 +450,11 @@ struct Chain {
     const Frag x0 = to_b(x[0], x[1]), x1 = to_b(x[2], x[3]);
     f32x4 U[4] = {zero, zero, zero, zero};
 #pragma unroll
-    for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(th[f], (kLk[f] ? x1 : x0).hi, U[kLm[f]]);
+    for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(get(th, R::T, f), (kLk[f] ? x1 : x0).hi, U[kLm[f]]);
 #pragma unroll
-    for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(th[f], (kLk[f] ? x1 : x0).lo, U[kLm[f]]);
+    for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(get(th, R::T, f), (kLk[f] ? x1 : x0).lo, U[kLm[f]]);
 #pragma unroll
-    for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(tl[f], (kLk[f] ? x1 : x0).hi, U[kLm[f]]);
+    for (int f = 0; f < 6; ++f) U[kLm[f]] = mma(get(tl, R::T + 6, f), (kLk[f] ? x1 : x0).hi, U[kLm[f]]);
     load_t(p, w, next);
     f32x4 D[4];
 #pragma unroll
@@ -444,13 +463,13 @@ struct Chain {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) S[mt] *= elc;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(kt[2 * mt], d0.hi, S[mt]);
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get(kt, R::KT, 2 * mt), d0.hi, S[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(kt[2 * mt], d0.lo, S[mt]);
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get(kt, R::KT, 2 * mt), d0.lo, S[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(kt[2 * mt + 1], d1.hi, S[mt]);
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get(kt, R::KT, 2 * mt + 1), d1.hi, S[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(kt[2 * mt + 1], d1.lo, S[mt]);
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get(kt, R::KT, 2 * mt + 1), d1.lo, S[mt]);
     if (NP == 2) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -458,7 +477,7 @@ struct Chain {
         S[mt] = mma(at<h8>(KT(p, w, c) + (NF + 2 * mt + 1) * kFrag, w.lane * 16), d1.hi, S[mt]);
       }
     }
-    load_frags(kt, KT(p, w, next), w.lane);
+    load(kt, KT(p, w, next), w.lane);
     on_u(to_b(U[0], U[1]), to_b(U[2], U[3]));
   }
   __device__ __forceinline__ void finish(const FwdArgs& p, const Place& w, float rsv) const {
@@ -471,21 +490,31 @@ struct Chain {
   }
 };
 
-template <Act A, int KP, bool SAVE>
+template <Act A, int KP, bool SAVE, bool RING>
 struct Output {
   static constexpr int NP = A == Act::F32 ? 2 : 1, KS = KP / 32, NF = KP / 8, PP = kPPlanes<A>;
   using Place = PassPlace<A>;
-  h8 qf[NF], pf[6];
+  using R = FwdRing<A, KP>;
+  h8 qf[RING ? 1 : NF], pf[RING ? 1 : 6];
   float eq;
   f32x4 y[4];
+  const uint16_t* ring;
+
+  template <int N>
+  __device__ __forceinline__ h8 get(const h8 (&x)[N], int base, int i) const {
+    if constexpr (RING) return ld8(ring + (base + i) * kFrag);
+    else return x[i];
+  }
 
   __device__ __forceinline__ const uint16_t* QF(const FwdArgs& p, const Place& w, int64_t c) const { return p.w.QF + (w.bg * w.nc + c) * (NP * NF * kFrag); }
   __device__ __forceinline__ const uint16_t* P(const FwdArgs& p, const Place& w, int64_t c) const { return p.w.P + (w.bh * w.nc + c) * (PP * 6 * kFrag); }
   __device__ __forceinline__ void load_q(const FwdArgs& p, const Place& w, int64_t c) {
-    load_frags(qf, QF(p, w, c), w.lane);
+    if constexpr (!RING) load_frags(qf, QF(p, w, c), w.lane);
     eq = p.w.hsc[(w.bh * w.nc + c) * (kHeadSc * kC) + H_EQ * kC + w.lane] * p.d.pscale;
   }
-  __device__ __forceinline__ void load_p(const FwdArgs& p, const Place& w, int64_t c) { load_frags(pf, P(p, w, c), w.lane); }
+  __device__ __forceinline__ void load_p(const FwdArgs& p, const Place& w, int64_t c) {
+    if constexpr (!RING) load_frags(pf, P(p, w, c), w.lane);
+  }
   __device__ __forceinline__ void begin(const Place& w, float* s) {
     mscan::wave_lds_sync();
     s[w.lane] = eq;
@@ -496,10 +525,10 @@ struct Output {
   __device__ __forceinline__ void state(const FwdArgs& p, const Place& w, int64_t c, int ks, const Frag& f) {
     if (SAVE) store_packed(p.w.S + ((w.bh * w.nc + c) * KP + 32 * ks) * p.d.VP, (4 * w.g * p.d.VP + w.col) * 4, f, p.d.VP);
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) y[mt] = mma(qf[mt * KS + ks], f.hi, y[mt]);
+    for (int mt = 0; mt < 4; ++mt) y[mt] = mma(get(qf, R::QF, mt * KS + ks), f.hi, y[mt]);
     if (PP == 2) {
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) y[mt] = mma(qf[mt * KS + ks], f.lo, y[mt]);
+      for (int mt = 0; mt < 4; ++mt) y[mt] = mma(get(qf, R::QF, mt * KS + ks), f.lo, y[mt]);
     }
     if (NP == 2) {
 #pragma unroll
@@ -517,12 +546,12 @@ struct Output {
       store_packed(p.w.U + (ci * kC + 32) * p.d.VP, off, u1, p.d.VP);
     }
 #pragma unroll
-    for (int f = 0; f < 6; ++f) y[kLm[f]] = mma(pf[f], (kLk[f] ? u1 : u0).hi, y[kLm[f]]);
+    for (int f = 0; f < 6; ++f) y[kLm[f]] = mma(get(pf, R::P, f), (kLk[f] ? u1 : u0).hi, y[kLm[f]]);
     if (PP == 2) {
 #pragma unroll
       for (int f = 0; f < 6; ++f) {
-        y[kLm[f]] = mma(pf[f], (kLk[f] ? u1 : u0).lo, y[kLm[f]]);
-        y[kLm[f]] = mma(at<h8>(P(p, w, c) + (6 + f) * kFrag, w.lane * 16), (kLk[f] ? u1 : u0).hi, y[kLm[f]]);
+        y[kLm[f]] = mma(get(pf, R::P, f), (kLk[f] ? u1 : u0).lo, y[kLm[f]]);
+        y[kLm[f]] = mma(RING ? ld8(ring + (R::P + 6 + f) * kFrag) : at<h8>(P(p, w, c) + (6 + f) * kFrag, w.lane * 16), (kLk[f] ? u1 : u0).hi, y[kLm[f]]);
       }
     }
     load_p(p, w, next);
@@ -532,6 +561,13 @@ struct Output {
   }
 };
 
+// the head's power of two: |s|, |v - S k| <= 2 sqrt(T + 1) max(|v|, |h0|) scaled below 2^15
+__device__ __forceinline__ float head_scale(const FwdArgs& p, int64_t bh, int lane) {
+  float m = 0.0f;
+  for (int64_t i = lane; i < p.d.nc; i += 64) m = fmaxf(m, p.w.vmax[bh * p.d.nc + i]);
+  return pow2_below(wave_max(m), 15 - static_cast<int>(ceilf(1.0f + 0.5f * log2f(static_cast<float>(p.d.T) + 1.0f))));
+}
+
 template <Act A, int KP, bool SAVE, bool PAIR>
 __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdArgs p) {
   constexpr int KS = KP / 32;
@@ -539,16 +575,13 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
   __shared__ __attribute__((aligned(16))) float s[4][kC];   // beta sv; beta e rk; exp(G_63 - G) rk / e rq pscale
   const Dims& d = p.d;
   const PassPlace<A> w(d);
-  // the head's power of two: |s|, |v - S k| <= 2 sqrt(T + 1) max(|v|, |h0|) scaled below 2^15
-  float m = 0.0f;
-  for (int64_t i = w.lane; i < d.nc; i += 64) m = fmaxf(m, p.w.vmax[w.bh * d.nc + i]);
-  const float sv = pow2_below(wave_max(m), 15 - static_cast<int>(ceilf(1.0f + 0.5f * log2f(static_cast<float>(d.T) + 1.0f))));
+  const float sv = head_scale(p, w.bh, w.lane);
   const float rsv = 1.0f / sv, yscale = rsv / d.pscale;
   if (SAVE && threadIdx.x == 0 && w.col < 16) p.w.sv[w.bh] = sv;
   if constexpr (PAIR) {
     __shared__ __attribute__((aligned(16))) PassBuf<KP> buf[2];
     if (wave_id() == 0) {
-      Chain<A, KP> ch;
+      Chain<A, KP, false> ch;
       ch.init(p, w, sv);
       for (int64_t c = 0; c < d.nc; ++c) {
         PassBuf<KP>& o = buf[c & 1];
@@ -569,7 +602,7 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
       }
       ch.finish(p, w, rsv);
     } else {
-      Output<A, KP, SAVE> out;
+      Output<A, KP, SAVE, false> out;
       out.load_q(p, w, 0);
       out.load_p(p, w, 0);
       for (int64_t c = 0; c < d.nc; ++c) {
@@ -594,8 +627,8 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
       }
     }
   } else {
-    Chain<A, KP> ch;
-    Output<A, KP, SAVE> out;
+    Chain<A, KP, false> ch;
+    Output<A, KP, SAVE, false> out;
     ch.init(p, w, sv);
     out.load_q(p, w, 0);
     out.load_p(p, w, 0);
@@ -606,6 +639,64 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
     }
     ch.finish(p, w, rsv);
   }
+}
+
+// The same for many tiles: four waves with a tile of one head each, and four that copy the chunk's fragments into LDS
+// (66 KB for d_k = 128 and bf16, twice) a chunk ahead.  A CU takes about 12 bytes a clock from L2 here, so what bounds
+// the kernel above, once it has several waves a CU, is every wave loading its own copy.
+constexpr int kRingTiles = 4;
+
+template <Act A, int KP, bool SAVE>
+__global__ void __launch_bounds__(512) gdelta_fwd_ring_kernel(const FwdArgs p) {
+  using R = FwdRing<A, KP>;
+  constexpr int NF = R::NF;
+  __shared__ __attribute__((aligned(16))) uint16_t ring[2][R::N * kFrag];
+  __shared__ __attribute__((aligned(16))) float s[kRingTiles][4][kC];
+  static_assert(sizeof(ring) + sizeof(s) <= mscan::kLdsBytes, "LDS");
+  const Dims& d = p.d;
+  const int wv = wave_id();
+  const PassPlace<A> w(d, kRingTiles, wv & (kRingTiles - 1));
+  if (wv >= kRingTiles) {
+    const int first = wv - kRingTiles;
+    auto copy = [&](int64_t c) {
+      uint16_t* dst = ring[c & 1];
+      const int64_t gi = w.bg * d.nc + c, ci = w.bh * d.nc + c;
+      copy_frags<NF, kRingTiles>(dst + R::KF * kFrag, p.w.KF + gi * (NF * kFrag), first, w.lane);
+      copy_frags<NF, kRingTiles>(dst + R::QF * kFrag, p.w.QF + gi * (NF * kFrag), first, w.lane);
+      copy_frags<12, kRingTiles>(dst + R::T * kFrag, p.w.T + ci * (12 * kFrag), first, w.lane);
+      copy_frags<NF, kRingTiles>(dst + R::KT * kFrag, p.w.KT + gi * (NF * kFrag), first, w.lane);
+      copy_frags<6 * kPPlanes<A>, kRingTiles>(dst + R::P * kFrag, p.w.P + ci * (6 * kPPlanes<A> * kFrag), first, w.lane);
+      wait_copies();
+    };
+    copy(0);
+    mscan::lds_barrier();
+    for (int64_t c = 0; c < d.nc; ++c) {
+      if (c + 1 < d.nc) copy(c + 1);
+      mscan::lds_barrier();   // chunk c + 1 is there, and chunk c's readers are done
+    }
+    return;
+  }
+  const float sv = head_scale(p, w.bh, w.lane);
+  const float rsv = 1.0f / sv, yscale = rsv / d.pscale;
+  if (SAVE && threadIdx.x == 0 && w.col < 16) p.w.sv[w.bh] = sv;
+  Chain<A, KP, true> ch;
+  Output<A, KP, SAVE, true> out;
+  const bool live = w.col < d.VP;   // a head's last workgroup may have tiles behind its columns
+  if (live) {
+    ch.init(p, w, sv);
+    out.load_q(p, w, 0);
+  }
+  mscan::lds_barrier();
+  for (int64_t c = 0; c < d.nc; ++c) {
+    if (live) {
+      ch.ring = out.ring = ring[c & 1] + w.lane * 8;
+      out.begin(w, s[wv][3]);
+      ch.step(p, w, c, sv, s[wv], [&](int ks, const Frag& f) { out.state(p, w, c, ks, f); },
+              [&](const Frag& u0, const Frag& u1) { out.u(p, w, c, yscale, s[wv][3], u0, u1); });
+    }
+    mscan::lds_barrier();
+  }
+  if (live) ch.finish(p, w, rsv);
 }
 
 // ------------------------------------------------------------------ token by token
@@ -742,9 +833,13 @@ hipError_t launch_chunks(const FwdArgs& a, bool save, hipStream_t st) {
   if (tiles <= kPairTiles) {
     if (save) hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, true, true>), dim3(tiles), dim3(128), 0, st, a);
     else hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, false, true>), dim3(tiles), dim3(128), 0, st, a);
-  } else {
+  } else if constexpr (A == Act::F32) {   // two planes a family: a chunk's fragments twice are more than the LDS
     if (save) hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, true, false>), dim3(tiles), dim3(64), 0, st, a);
     else hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, false, false>), dim3(tiles), dim3(64), 0, st, a);
+  } else {
+    const dim3 grid(bh * ((d.VP / 16 + kRingTiles - 1) / kRingTiles));
+    if (save) hipLaunchKernelGGL((gdelta_fwd_ring_kernel<A, KP, true>), grid, dim3(512), 0, st, a);
+    else hipLaunchKernelGGL((gdelta_fwd_ring_kernel<A, KP, false>), grid, dim3(512), 0, st, a);
   }
   return hipGetLastError();
 }

@@ -90,6 +90,19 @@ def test_forward_and_backward(mscan, shape, act, h0):
 
 
 @pytest.mark.parametrize("act", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shape", [(6, 70, 24, 24, 40, 80), (9, 130, 16, 8, 120, 64)], ids=str)
+def test_many_heads(mscan, shape, act):
+    """More 16-column tiles than waves: the passes that share a head's operands (a workgroup of the first shape has tiles
+    behind the columns)."""
+    x, ref = make(*shape, act, seed=29)
+    train(mscan, (*shape, act), x, ref, h0=True)
+    core = mscan.GatedDeltaCore(dims_of(mscan, *shape, act), train=False)
+    core.forward(x, h0=x["h0"])
+    y, last = og.forward(**{n: ref[n] for n in NAMES}, h0=ref["h0"])
+    check(dict(y=(core.y, y), h_last=(core.h_last, last)))
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("T", [1, 15, 16, 17, 64, 100, 257])
 def test_forward_alone(mscan, act, T):
     """Without anything kept: the short sequences' token-by-token kernel and the chunks; h_last over h0."""
