@@ -244,8 +244,9 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
 // ------------------------------------------------------------------ the chunks' own gradients
 // One workgroup per (batch row, query / key head, chunk), over the value heads that share it.  First all products
 // with d_v contracted, in slabs of 32 columns: rows of dO, U and Y through LDS (the next slab's in flight), S and dS'
-// from global memory straight into the fragments of the wave that owns their d_k rows.  Then the 64 x 64 gradients M1
-// and M2 (ten lower tiles over the four waves), and their products with q and k.
+// from global memory straight into the fragments of the wave that owns their d_k rows.  Then the 64 x 64 gradients
+// M1 and M2 (ten lower tiles over the waves), and their products with q and k.  Bound by HBM: per chunk and head 300 KB
+// at d_k = d_v = 128, S, dS', U and Y being 192 of them.
 constexpr int kSlab = 32 + 8;
 
 template <Act A>
@@ -255,78 +256,100 @@ struct ChunkLds {
     struct {
       uint16_t dO[NP][kC * kSlab], U[2][kC * kSlab], Y[2][kC * kSlab];
     } slab[2];
-    struct {
-      uint16_t M1[2][kC * kCol], M1T[2][kC * kCol], M2[2][kC * kCol], M2T[2][kC * kCol];
-    };
+    uint16_t M[8][kC * kCol];   // high and low parts of M1, its transpose, M2, its transpose
   };
-  double G[kC];
+  double G[kC], rowE[10][16], colE[10][16];   // E's sums, by lower tile
   float beta[kC], e[kC], dec[kC], rk[kC], rq[kC], db[kC];
-  float rowE[4][kC], colE[4][kC];   // by column tile, by row tile
-  float rows[4][3][kC];             // by wave
-  float red[8];
-};
+  float red[2][8];
 
-__device__ __forceinline__ void unpack8(u32x4 a, u32x4 b, h8& hi, h8& lo) {
-  u32x4 h, l;
-  h[0] = (a[0] & 0xffffu) | (a[1] << 16);
-  h[1] = (a[2] & 0xffffu) | (a[3] << 16);
-  h[2] = (b[0] & 0xffffu) | (b[1] << 16);
-  h[3] = (b[2] & 0xffffu) | (b[3] << 16);
-  l[0] = (a[0] >> 16) | (a[1] & 0xffff0000u);
-  l[1] = (a[2] >> 16) | (a[3] & 0xffff0000u);
-  l[2] = (b[0] >> 16) | (b[1] & 0xffff0000u);
-  l[3] = (b[2] >> 16) | (b[3] & 0xffff0000u);
-  hi = __builtin_bit_cast(h8, h);
-  lo = __builtin_bit_cast(h8, l);
+  // four floats in the padding of row i of plane n: the waves' row sums
+  __device__ __forceinline__ f32x4& pad(int n, int i) { return *reinterpret_cast<f32x4*>(M[n] + i * kCol + kC); }
+};
+enum { M_1 = 0, M_1T = 2, M_2 = 4, M_2T = 6 };
+
+__device__ __forceinline__ u32x2 low_halves(u32x4 a) {   // of packed words: the high parts of four values
+  return u32x2{__builtin_amdgcn_perm(a[1], a[0], 0x05040100), __builtin_amdgcn_perm(a[3], a[2], 0x05040100)};
 }
+__device__ __forceinline__ u32x2 high_halves(u32x4 a) {
+  return u32x2{__builtin_amdgcn_perm(a[1], a[0], 0x07060302), __builtin_amdgcn_perm(a[3], a[2], 0x07060302)};
+}
+__device__ __forceinline__ h8 join(u32x2 a, u32x2 b) { return __builtin_bit_cast(h8, (u32x4{a[0], a[1], b[0], b[1]})); }
+
+// lower tile number n of ten: row tile, column tile
+__device__ __forceinline__ int lower_row(int n) { return n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3; }
+__device__ __forceinline__ int lower_col(int n) { return n - lower_row(n) * (lower_row(n) + 1) / 2; }
 
 template <Act A, int KP, bool SHARED>
-__global__ void __launch_bounds__(256, SHARED ? 1 : 2) gdelta_bwd_chunk_kernel(const BwdArgs p) {
-  constexpr int NP = A == Act::F32 ? 2 : 1, NT = KP / 64, KS = KP / 32, NF = KP / 8;
+__global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs p) {
+  constexpr int NP = A == Act::F32 ? 2 : 1, KS = KP / 32, NF = KP / 8, NW = 4, NTHR = NW * 64, NT = KP / 64;   // NT tiles of 16 d_k rows to a wave
+  constexpr int CPT = 64 * 32 / NTHR, SUB = CPT / 4, TILES = (10 + NW - 1) / NW;   // a thread's columns of a slab, in fours
   __shared__ __attribute__((aligned(16))) ChunkLds<A> s;
   static_assert(sizeof(s) <= mscan::kLdsBytes / 2, "two workgroups a CU");
   const Dims& d = p.d;
   const int tid = threadIdx.x, lane = tid & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
-  const int64_t c = blockIdx.x % d.nc, bg = blockIdx.x / d.nc, hk = bg % d.G, b = bg / d.G;
+  const uint32_t nc32 = static_cast<uint32_t>(d.nc), G32 = static_cast<uint32_t>(d.G);
+  const int64_t c = blockIdx.x % nc32, bg = blockIdx.x / nc32, hk = bg % G32, b = static_cast<uint32_t>(bg) / G32;
   const int64_t t0 = c * kC, left = d.T - t0, gi = bg * d.nc + c;
   const int share = SHARED ? static_cast<int>(d.H / d.G) : 1;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  const int n0 = wv * NT;   // this wave's d_k tiles: n0 .. n0 + NT - 1
   const float* gsc = p.w.gsc + gi * (kGroupSc * kC);
-  const uint16_t* KF = p.w.KF + gi * (NP * NF * kFrag);
-  const uint16_t* QF = p.w.QF + gi * (NP * NF * kFrag);
-  const uint16_t* KT = p.w.KT + gi * (NP * NF * kFrag);
-  const uint16_t* QT = p.w.QT + gi * (NP * NF * kFrag);
   f32x4 totQ[4][NT], totK[4][NT];
-  h8 kt[NP][NT][2], qt[NP][NT][2];   // elements 0 .. 3: token rows 4 g + e of tile 2 ks, 4 .. 7: of tile 2 ks + 1
+  h8 kt[NT][NP][2], qt[NT][NP][2];   // elements 0 .. 3: token rows 4 g + e of tile 2 ks, 4 .. 7: of tile 2 ks + 1
+  auto elem = [](const h8 (&x)[NP][2], int mt, int e, float f, float acc) {   // acc + f x, of the parts as they are
+    acc = fmaf(f, static_cast<float>(x[0][mt >> 1][(mt & 1) * 4 + e]), acc);
+    if (NP == 2) acc = fmaf(f, static_cast<float>(x[NP - 1][mt >> 1][(mt & 1) * 4 + e]), acc);
+    return acc;
+  };
 
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) totQ[mt][n] = totK[mt][n] = zero;
+#pragma clang loop unroll(disable)
   for (int hi_ = 0; hi_ < share; ++hi_) {
     const int64_t h = hk * share + hi_, bh = b * d.H + h, ci = bh * d.nc + c;
-    const float so = p.so[bh], rso = 1.0f / so, rsv = 1.0f / p.w.sv[bh];
-    f32x4 aP[3], aA[3], aQ[4][NT], aKq[4][NT], aKs[4][NT];
+    int64_t fo = gi * (NP * NF * kFrag);
+    if (SHARED) asm volatile("" : "+s"(fo));   // or the heads' loop keeps every fragment of k and q in registers
+    const uint16_t* KF = p.w.KF + fo;
+    const uint16_t* QF = p.w.QF + fo;
+    const uint16_t* KT = p.w.KT + fo;
+    const uint16_t* QT = p.w.QT + fo;
+    const float so = p.so[bh], rs1 = 1.0f / so, rs2 = 1.0f / p.w.sv[bh];   // two factors: their product may leave f32's range
+    f32x4 aP[TILES], aA[TILES], aQ[4][NT], aKq[4][NT], aKs[4][NT];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) aP[i] = aA[i] = zero;
+    for (int i = 0; i < TILES; ++i) aP[i] = aA[i] = zero;
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int n = 0; n < NT; ++n) aQ[mt][n] = aKq[mt][n] = aKs[mt][n] = zero;
     float dot = 0.0f;   // <dS', S>
-    // a thread's part of a slab: 8 columns of one token
-    const int t = tid >> 2, cc = (tid & 3) * 8;
-    u32x4 ru[2], ry[2], ro[NP], rs[NT][2], rd[NT][2];
-    const uint32_t uoff = (t * d.VP + cc) * 4, soff = (r * d.VP + 8 * g) * 4;
-    const char* dyb = static_cast<const char*>(p.dy) + ((b * d.T + t0) * d.H + h) * (d.V * (NP * 2));
-    const uint32_t dyoff = (static_cast<uint32_t>(t) * static_cast<uint32_t>(d.H * d.V) + cc) * (NP * 2);
+    const int t = tid / (32 / CPT), cc = tid % (32 / CPT) * CPT;
+    u32x4 ru[SUB], ry[SUB], rs[NT][2], rd[NT][2];
+    uint32_t ro[SUB][NP * 2];
+    const Buf bu = buf_of(p.w.U + ci * kC * d.VP), by = buf_of(p.DU + ci * kC * d.VP);
+    const Buf bs = buf_of(p.w.S + (ci * KP + 16 * NT * wv) * d.VP), bd = buf_of(p.DS + (ci * KP + 16 * NT * wv) * d.VP);
+    const Buf bo = buf_of(static_cast<const char*>(p.dy) + ((b * d.T + t0) * d.H + h) * (d.V * (NP * 2)));
+    const int uoff = (t * d.VP + cc) * 4, soff = (r * d.VP + 8 * g) * 4;
+    const int ooff = (t * static_cast<int>(d.H) * d.V + cc) * (NP * 2);
     auto load_rows = [&](int v0) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        ru[i] = at<u32x4>(p.w.U + ci * kC * d.VP + v0 + 4 * i, uoff);
-        ry[i] = at<u32x4>(p.DU + ci * kC * d.VP + v0 + 4 * i, uoff);
-      }
+      for (int i = 0; i < SUB; ++i) {
+        ru[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(bu, uoff + 16 * i, v0 * 4, 0));
+        ry[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(by, uoff + 16 * i, v0 * 4, 0));
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        ro[i] = u32x4{0u, 0u, 0u, 0u};
-        if (t < left && v0 + cc < d.V) ro[i] = at<u32x4>(dyb + v0 * (NP * 2) + 16 * i, dyoff);
+        for (int k = 0; k < NP * 2; ++k) ro[i][k] = 0u;
+        if (t < left && v0 + cc + 4 * i < d.V) {
+          const int at_ = ooff + i * NP * 8;
+          if constexpr (NP == 2) {
+            const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(bo, at_, v0 * 4, 0));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ro[i][k] = x[k];
+          } else {
+            const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(bo, at_, v0 * 2, 0));
+            ro[i][0] = x[0];
+            ro[i][1] = x[1];
+          }
+        }
       }
     };
     auto load_states = [&](int v0) {
@@ -334,8 +357,8 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) gdelta_bwd_chunk_kernel(c
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          rs[n][i] = at<u32x4>(p.w.S + (ci * KP + 16 * (n0 + n)) * d.VP + v0 + 4 * i, soff);
-          rd[n][i] = at<u32x4>(p.DS + (ci * KP + 16 * (n0 + n)) * d.VP + v0 + 4 * i, soff);
+          rs[n][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(bs, soff + 16 * i, (v0 + 16 * n * d.VP) * 4, 0));
+          rd[n][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(bd, soff + 16 * i, (v0 + 16 * n * d.VP) * 4, 0));
         }
     };
     load_rows(0);
@@ -352,50 +375,52 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) gdelta_bwd_chunk_kernel(c
     }
     for (int v0 = 0; v0 < d.VP; v0 += 32) {
       auto& sl = s.slab[(v0 >> 5) & 1];
-      {
-        h8 ph, pl;
-        unpack8(ru[0], ru[1], ph, pl);
-        *reinterpret_cast<h8*>(sl.U[0] + t * kSlab + cc) = ph;
-        *reinterpret_cast<h8*>(sl.U[1] + t * kSlab + cc) = pl;
-        unpack8(ry[0], ry[1], ph, pl);
-        *reinterpret_cast<h8*>(sl.Y[0] + t * kSlab + cc) = ph;
-        *reinterpret_cast<h8*>(sl.Y[1] + t * kSlab + cc) = pl;
-        u32x4 hi, lo;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+      for (int i = 0; i < SUB; ++i) {
+        const int at_ = t * kSlab + cc + 4 * i;
+        *reinterpret_cast<u32x2*>(sl.U[0] + at_) = low_halves(ru[i]);
+        *reinterpret_cast<u32x2*>(sl.U[1] + at_) = high_halves(ru[i]);
+        *reinterpret_cast<u32x2*>(sl.Y[0] + at_) = low_halves(ry[i]);
+        *reinterpret_cast<u32x2*>(sl.Y[1] + at_) = high_halves(ry[i]);
+        u32x2 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
           float x, y;
           if constexpr (NP == 2) {
-            x = __builtin_bit_cast(float, static_cast<uint32_t>(ro[e >> 1][(e & 1) * 2]));
-            y = __builtin_bit_cast(float, static_cast<uint32_t>(ro[e >> 1][(e & 1) * 2 + 1]));
+            x = __builtin_bit_cast(float, ro[i][2 * e]);
+            y = __builtin_bit_cast(float, ro[i][2 * e + 1]);
           } else {
-            x = IO<A>::cvt(ro[0][e] & 0xffffu);
-            y = IO<A>::cvt(ro[0][e] >> 16);
+            x = IO<A>::cvt(ro[i][e] & 0xffffu);
+            y = IO<A>::cvt(ro[i][e] >> 16);
           }
           uint32_t a, bb;
           split2(x * so, y * so, a, bb);
           hi[e] = a;
           lo[e] = bb;
         }
-        *reinterpret_cast<u32x4*>(sl.dO[0] + t * kSlab + cc) = hi;
-        if (NP == 2) *reinterpret_cast<u32x4*>(sl.dO[NP - 1] + t * kSlab + cc) = lo;
+        *reinterpret_cast<u32x2*>(sl.dO[0] + at_) = hi;
+        if (NP == 2) *reinterpret_cast<u32x2*>(sl.dO[NP - 1] + at_) = lo;
       }
       h8 sh[NT], slo[NT], gh[NT], gl[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        unpack8(rs[n][0], rs[n][1], sh[n], slo[n]);
-        unpack8(rd[n][0], rd[n][1], gh[n], gl[n]);
+        sh[n] = join(low_halves(rs[n][0]), low_halves(rs[n][1]));
+        slo[n] = join(high_halves(rs[n][0]), high_halves(rs[n][1]));
+        gh[n] = join(low_halves(rd[n][0]), low_halves(rd[n][1]));
+        gl[n] = join(high_halves(rd[n][0]), high_halves(rd[n][1]));
       }
-      if (v0 + 32 < d.VP) {
-        load_rows(v0 + 32);
-        load_states(v0 + 32);
-      }
+      const int next = v0 + 32 < d.VP ? v0 + 32 : v0;   // the last slab loads its own again: no branch
+      load_rows(next);
+      load_states(next);
       mscan::lds_barrier();
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          dot = fmaf(static_cast<float>(sh[n][e]) + static_cast<float>(slo[n][e]),
-                     static_cast<float>(gh[n][e]) + static_cast<float>(gl[n][e]), dot);
+        for (int e = 0; e < 8; ++e) {
+          dot = fmaf(static_cast<float>(sh[n][e]), static_cast<float>(gh[n][e]), dot);
+          dot = fmaf(static_cast<float>(sh[n][e]), static_cast<float>(gl[n][e]), dot);
+          dot = fmaf(static_cast<float>(slo[n][e]), static_cast<float>(gh[n][e]), dot);
+        }
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
         const int a = (16 * mt + r) * kSlab + 8 * g;
@@ -415,17 +440,16 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) gdelta_bwd_chunk_kernel(c
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+          if (NP == 2) aQ[mt][n] = mma(ld8(sl.dO[NP - 1] + a), sh[n], aQ[mt][n]);
           aKq[mt][n] = mma(yl, sh[n], aKq[mt][n]);
           aKs[mt][n] = mma(ul, gh[n], aKs[mt][n]);
-          if (NP == 2) aQ[mt][n] = mma(ld8(sl.dO[NP - 1] + a), sh[n], aQ[mt][n]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {   // lower tiles wv, wv + 4, wv + 8
-        const int tl = wv + 4 * i;
+      for (int i = 0; i < TILES; ++i) {   // lower tiles wv, wv + NW, ..
+        const int tl = wv + NW * i;
         if (tl >= 10) break;
-        const int mt = tl < 1 ? 0 : tl < 3 ? 1 : tl < 6 ? 2 : 3, nt = tl - mt * (mt + 1) / 2;
-        const int a = (16 * mt + r) * kSlab + 8 * g, bb = (16 * nt + r) * kSlab + 8 * g;
+        const int a = (16 * lower_row(tl) + r) * kSlab + 8 * g, bb = (16 * lower_col(tl) + r) * kSlab + 8 * g;
         const h8 oh = ld8(sl.dO[0] + a), yh = ld8(sl.Y[0] + a), yl = ld8(sl.Y[1] + a);
         const h8 uh = ld8(sl.U[0] + bb), ul = ld8(sl.U[1] + bb);
         aP[i] = mma(oh, uh, aP[i]);
@@ -437,211 +461,211 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) gdelta_bwd_chunk_kernel(c
       }
     }
 #pragma unroll
-    for (int pl = 0; pl < NP; ++pl)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int pl = 0; pl < NP; ++pl)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          kt[pl][n][ks] = at<h8>(KT + (pl * NF + 2 * (n0 + n) + ks) * kFrag, lane * 16);
-          qt[pl][n][ks] = at<h8>(QT + (pl * NF + 2 * (n0 + n) + ks) * kFrag, lane * 16);
+          kt[n][pl][ks] = at<h8>(KT + (pl * NF + 2 * (NT * wv + n) + ks) * kFrag, lane * 16);
+          qt[n][pl][ks] = at<h8>(QT + (pl * NF + 2 * (NT * wv + n) + ks) * kFrag, lane * 16);
         }
     // this wave's tiles of the 64 x 64 gradients, and of E
-    f32x4 m1[3], m2[3];
+    f32x4 m1[TILES], m2[TILES];
     float big = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < TILES; ++i) {
       m1[i] = m2[i] = zero;
-      const int tl = wv + 4 * i;
+      const int tl = wv + NW * i;
       if (tl >= 10) break;
-      const int mt = tl < 1 ? 0 : tl < 3 ? 1 : tl < 6 ? 2 : 3, nt = tl - mt * (mt + 1) / 2, j = 16 * nt + r;
+      const int mt = lower_row(tl), nt = lower_col(tl), j = 16 * nt + r, i0 = 16 * mt + 4 * g;
       const f32x4 kq = frag_mm<NP, KS, NF>(QF + mt * KS * kFrag, KF + nt * KS * kFrag, lane, zero);
       const f32x4 kk = frag_mm<NP, KS, NF>(KF + mt * KS * kFrag, KF + nt * KS * kFrag, lane, zero);
+      const f32x4 rq = *reinterpret_cast<const f32x4*>(s.rq + i0), rk = *reinterpret_cast<const f32x4*>(s.rk + i0);
+      const f32x4 be = *reinterpret_cast<const f32x4*>(s.beta + i0);
       const float rkj = s.rk[j];
       const double Gj = s.G[j];
-      float ce = 0.0f;
+      double ce = 0.0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int ti = 16 * mt + 4 * g + e;
-        const float rq = s.rq[ti], rk = s.rk[ti], be = s.beta[ti];
+        const int ti = i0 + e;
         const float D = j <= ti ? exp2_fast(static_cast<float>(s.G[ti] - Gj)) : 0.0f;
-        const float dP = aP[i][e] * rso * rsv, yu = aA[i][e] * rso * rsv;
+        const float dP = aP[i][e] * rs1 * rs2, yu = aA[i][e] * rs1 * rs2;
         float E = 0.0f;
         m1[i][e] = j <= ti ? dP * D : 0.0f;
         if (j < ti) {
-          m2[i][e] = -yu * be * D;
-          E = m1[i][e] * (rq * rkj * kq[e]) + m2[i][e] * (rk * rkj * kk[e]);
+          m2[i][e] = -yu * be[e] * D;
+          E = m1[i][e] * (rq[e] * rkj * kq[e]) + m2[i][e] * (rk[e] * rkj * kk[e]);
         }
-        if (ti == j) s.db[ti] = yu * (1.0f - be);
-        ce += E;
-        const float re = sum16(E);
-        if (r == 0) s.rowE[nt][ti] = re;
-        big = max_finite(big, fmaxf(fabsf(m1[i][e]), fabsf(m2[i][e])) * fmaxf(rkj, fmaxf(fabsf(rq), rk)));
+        if (ti == j) s.db[ti] = yu * (1.0f - be[e]);
+        // the sums over rows and over columns cancel where a token's g stands between neither or both of a pair: in
+        // f64 they do so to the last bit of E
+        ce += static_cast<double>(E);
+        const double re = sum16(static_cast<double>(E));
+        if (r == 0) s.rowE[tl][4 * g + e] = re;
+        big = max_finite(big, fmaxf(fabsf(m1[i][e]), fabsf(m2[i][e])) * fmaxf(rkj, fmaxf(fabsf(rq[e]), rk[e])));
       }
       ce += __shfl_xor(ce, 16, 64);
       ce += __shfl_xor(ce, 32, 64);
-      if (g == 0) s.colE[mt][j] = ce;
+      if (g == 0) s.colE[tl][r] = ce;
     }
     big = wave_max(big);
     dot = wave_sum(dot);
     if (lane == 0) {
-      s.red[wv] = big;
-      s.red[4 + wv] = dot;
+      s.red[0][wv] = big;
+      s.red[1][wv] = dot;
     }
     __syncthreads();   // the slabs are read, s.red written
-    const float sm = pow2_below(fmaxf(fmaxf(s.red[0], s.red[1]), fmaxf(s.red[2], s.red[3])), 13), rsm = 1.0f / sm;
-    dot = (s.red[4] + s.red[5]) + (s.red[6] + s.red[7]);
-    {   // zeros in the tiles past the diagonal that a 32-wide step reads: (0, 1), (2, 3), and (1, 0), (3, 2) of the transposes
+    big = dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      big = fmaxf(big, s.red[0][i]);
+      dot += s.red[1][i];
+    }
+    const float sm = pow2_below(big, 13), rsm = 1.0f / sm;
+    if (tid < 256) {   // zeros in the tiles past the diagonal that a 32-wide step reads: (0, 1), (2, 3), and (1, 0), (3, 2) of the transposes
       const int pl = tid >> 7, tile = (tid >> 6) & 1, row = (tid >> 2) & 15, q = tid & 3;
       const int up = (32 * tile + row) * kCol + 32 * tile + 8 * q + 4, dn = (32 * tile + 16 + row) * kCol + 32 * tile + 8 * q;
-      *reinterpret_cast<u32x2*>(s.M1[pl] + up) = u32x2{0u, 0u};
-      *reinterpret_cast<u32x2*>(s.M2[pl] + up) = u32x2{0u, 0u};
-      *reinterpret_cast<u32x2*>(s.M1T[pl] + dn) = u32x2{0u, 0u};
-      *reinterpret_cast<u32x2*>(s.M2T[pl] + dn) = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(s.M[M_1 + pl] + up) = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(s.M[M_2 + pl] + up) = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(s.M[M_1T + pl] + dn) = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(s.M[M_2T + pl] + dn) = u32x2{0u, 0u};
     }
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const int tl = wv + 4 * i;
+    for (int i = 0; i < TILES; ++i) {
+      const int tl = wv + NW * i;
       if (tl >= 10) break;
-      const int mt = tl < 1 ? 0 : tl < 3 ? 1 : tl < 6 ? 2 : 3, nt = tl - mt * (mt + 1) / 2, j = 16 * nt + r, i0 = 16 * mt + 4 * g;
+      const int j = 16 * lower_col(tl) + r, i0 = 16 * lower_row(tl) + 4 * g;
       const float rkj = s.rk[j];
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
-        const f32x4 m = which ? m2[i] : m1[i];
-        const float* ri = (which ? s.rk : s.rq) + i0;
-        const int a = i0 * kCol + place(j), at_ = j * kCol + place(i0);
-        uint16_t* hp = which ? s.M2[0] : s.M1[0];
-        uint16_t* lp = which ? s.M2[1] : s.M1[1];
-        uint32_t th[2], tlo[2];
+        const f32x4 m = (which ? m2[i] : m1[i]) * sm, ri = *reinterpret_cast<const f32x4*>((which ? s.rk : s.rq) + i0);
+        uint16_t* hp = s.M[which ? M_2 : M_1] + i0 * kCol + place(j);
+        uint16_t* tp = s.M[which ? M_2T : M_1T] + j * kCol + place(i0);
+        u32x2 th, tlo;
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
-          const float x = m[2 * o] * sm, y = m[2 * o + 1] * sm;
-          uint32_t hh, ll;
-          split2(x * rkj, y * rkj, hh, ll);
-          split2(x * ri[2 * o], y * ri[2 * o + 1], th[o], tlo[o]);
-          hp[a + (2 * o) * kCol] = static_cast<uint16_t>(hh);
-          hp[a + (2 * o + 1) * kCol] = static_cast<uint16_t>(hh >> 16);
-          lp[a + (2 * o) * kCol] = static_cast<uint16_t>(ll);
-          lp[a + (2 * o + 1) * kCol] = static_cast<uint16_t>(ll >> 16);
+          uint32_t hh, ll, x, y;
+          split2(m[2 * o] * rkj, m[2 * o + 1] * rkj, hh, ll);
+          split2(m[2 * o] * ri[2 * o], m[2 * o + 1] * ri[2 * o + 1], x, y);
+          th[o] = x;
+          tlo[o] = y;
+          hp[(2 * o) * kCol] = static_cast<uint16_t>(hh);
+          hp[(2 * o + 1) * kCol] = static_cast<uint16_t>(hh >> 16);
+          hp[kC * kCol + (2 * o) * kCol] = static_cast<uint16_t>(ll);
+          hp[kC * kCol + (2 * o + 1) * kCol] = static_cast<uint16_t>(ll >> 16);
         }
-        *reinterpret_cast<u32x2*>((which ? s.M2T[0] : s.M1T[0]) + at_) = u32x2{th[0], th[1]};
-        *reinterpret_cast<u32x2*>((which ? s.M2T[1] : s.M1T[1]) + at_) = u32x2{tlo[0], tlo[1]};
+        *reinterpret_cast<u32x2*>(tp) = th;
+        *reinterpret_cast<u32x2*>(tp + kC * kCol) = tlo;
       }
     }
     // the parts through the state, in true units, and their products with q and k for the decay's gradient
-    auto elem = [&](const h8 (&x)[NP][NT][2], int n, int mt, int e) {
-      float v = static_cast<float>(x[0][n][mt >> 1][(mt & 1) * 4 + e]);
-      if (NP == 2) v += static_cast<float>(x[NP - 1][n][mt >> 1][(mt & 1) * 4 + e]);
-      return v;
-    };
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int mt = 0; mt < 4; ++mt) {
+      const int i0 = 16 * mt + 4 * g;
+      const f32x4 ev = *reinterpret_cast<const f32x4*>(s.e + i0), be = *reinterpret_cast<const f32x4*>(s.beta + i0);
+      const f32x4 de = *reinterpret_cast<const f32x4*>(s.dec + i0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        aQ[mt][n] = aQ[mt][n] * (ev * rs1) * rs2;
+        aKq[mt][n] = aKq[mt][n] * (ev * be * -rs1) * rs2;
+        aKs[mt][n] = aKs[mt][n] * (de * rs1) * rs2;
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int ti = 16 * mt + 4 * g + e;
-        const float ev = s.e[ti], be = s.beta[ti], de = s.dec[ti];
         float wq = 0.0f, wkq = 0.0f, wks = 0.0f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          aQ[mt][n][e] *= ev * rso * rsv;
-          aKq[mt][n][e] *= -(ev * be) * rso * rsv;
-          aKs[mt][n][e] *= de * rso * rsv;
-          const float kv = elem(kt, n, mt, e);
-          wq = fmaf(aQ[mt][n][e], elem(qt, n, mt, e), wq);
-          wkq = fmaf(aKq[mt][n][e], kv, wkq);
-          wks = fmaf(aKs[mt][n][e], kv, wks);
+          wq = elem(qt[n], mt, e, aQ[mt][n][e], wq);
+          wkq = elem(kt[n], mt, e, aKq[mt][n][e], wkq);
+          wks = elem(kt[n], mt, e, aKs[mt][n][e], wks);
         }
         wq = sum16(wq);
         wkq = sum16(wkq);
         wks = sum16(wks);
-        if (r == 0) {
-          s.rows[wv][0][ti] = wq * s.rq[ti];
-          s.rows[wv][1][ti] = wkq * s.rk[ti];
-          s.rows[wv][2][ti] = wks * s.rk[ti];
-        }
+        if (r == 0) s.pad(wv, i0 + e) = f32x4{wq, wkq, wks, 0.0f};
       }
+    }
     mscan::lds_barrier();
     // the parts inside the chunk
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
       f32x4 q[NT], k[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          q[n][e] = aQ[mt][n][e] * sm;
-          k[n][e] = (aKq[mt][n][e] + aKs[mt][n][e]) * sm;
-        }
+      for (int n = 0; n < NT; ++n) {
+        q[n] = aQ[mt][n] * sm;
+        k[n] = (aKq[mt][n] + aKs[mt][n]) * sm;
+      }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const int a = (16 * mt + r) * kCol + 8 * g + 32 * ks;
         if (ks == 0 || mt >= 2) {   // rows i, columns j <= i
-          const h8 xh = ld8(s.M1[0] + a), xl = ld8(s.M1[1] + a), yh = ld8(s.M2[0] + a), yl = ld8(s.M2[1] + a);
+          const h8 xh = ld8(s.M[M_1] + a), xl = ld8(s.M[M_1 + 1] + a), yh = ld8(s.M[M_2] + a), yl = ld8(s.M[M_2 + 1] + a);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            q[n] = mma(xh, kt[0][n][ks], q[n]);
-            k[n] = mma(yh, kt[0][n][ks], k[n]);
-            q[n] = mma(xl, kt[0][n][ks], q[n]);
-            k[n] = mma(yl, kt[0][n][ks], k[n]);
+            q[n] = mma(xh, kt[n][0][ks], q[n]);
+            k[n] = mma(yh, kt[n][0][ks], k[n]);
+            q[n] = mma(xl, kt[n][0][ks], q[n]);
+            k[n] = mma(yl, kt[n][0][ks], k[n]);
             if (NP == 2) {
-              q[n] = mma(xh, kt[NP - 1][n][ks], q[n]);
-              k[n] = mma(yh, kt[NP - 1][n][ks], k[n]);
+              q[n] = mma(xh, kt[n][NP - 1][ks], q[n]);
+              k[n] = mma(yh, kt[n][NP - 1][ks], k[n]);
             }
           }
         }
         if (ks == 1 || mt < 2) {    // rows j, columns i >= j
-          const h8 xh = ld8(s.M1T[0] + a), xl = ld8(s.M1T[1] + a), yh = ld8(s.M2T[0] + a), yl = ld8(s.M2T[1] + a);
+          const h8 xh = ld8(s.M[M_1T] + a), xl = ld8(s.M[M_1T + 1] + a), yh = ld8(s.M[M_2T] + a), yl = ld8(s.M[M_2T + 1] + a);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            k[n] = mma(xh, qt[0][n][ks], k[n]);
-            k[n] = mma(xl, qt[0][n][ks], k[n]);
-            k[n] = mma(yh, kt[0][n][ks], k[n]);
-            k[n] = mma(yl, kt[0][n][ks], k[n]);
+            k[n] = mma(xh, qt[n][0][ks], k[n]);
+            k[n] = mma(xl, qt[n][0][ks], k[n]);
+            k[n] = mma(yh, kt[n][0][ks], k[n]);
+            k[n] = mma(yl, kt[n][0][ks], k[n]);
             if (NP == 2) {
-              k[n] = mma(xh, qt[NP - 1][n][ks], k[n]);
-              k[n] = mma(yh, kt[NP - 1][n][ks], k[n]);
+              k[n] = mma(xh, qt[n][NP - 1][ks], k[n]);
+              k[n] = mma(yh, kt[n][NP - 1][ks], k[n]);
             }
           }
         }
       }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          totQ[mt][n][e] = (SHARED && hi_ ? totQ[mt][n][e] : 0.0f) + q[n][e] * rsm;
-          totK[mt][n][e] = (SHARED && hi_ ? totK[mt][n][e] : 0.0f) + k[n][e] * rsm;
-        }
+      for (int n = 0; n < NT; ++n) {
+        totQ[mt][n] = SHARED ? totQ[mt][n] + q[n] * rsm : q[n] * rsm;
+        totK[mt][n] = SHARED ? totK[mt][n] + k[n] * rsm : k[n] * rsm;
+      }
     }
     if (tid < kC) {   // dg and what comes of it
       float x = 0.0f, z = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        x += s.rows[w][0][tid] + s.rows[w][1][tid];
-        z += s.rows[w][2][tid];
+      for (int w = 0; w < NW; ++w) {
+        const f32x4 v = s.pad(w, tid);
+        x += v[0] * s.rq[tid] + v[1] * s.rk[tid];
+        z += v[2] * s.rk[tid];
       }
-      float E = 0.0f, C = 0.0f;
+      double E = 0.0;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        if (w <= (tid >> 4)) E += s.rowE[w][tid];
-        if (w >= (tid >> 4)) C += s.colE[w][tid];
+      for (int n = 0; n < 10; ++n) {
+        if (lower_row(n) == (tid >> 4)) E += s.rowE[n][tid & 15];
+        if (lower_col(n) == (tid >> 4)) E -= s.colE[n][tid & 15];
       }
-      float dG = (E - C) + (x - z);
-      // suffix sum over the chunk's tokens
+      double dg = E + static_cast<double>(x);   // summed over this and the later tokens
+      float before = z;                         // and this over the earlier ones
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
-        const float up = __shfl_down(dG, o, 64);
-        if (tid + o < 64) dG += up;
+        const double up = __shfl_down(dg, o, 64);
+        const float dn = __shfl_up(before, o, 64);
+        if (tid + o < 64) dg += up;
+        if (tid >= o) before += dn;
       }
-      const float through = wave_sum(z) + s.e[kC - 1] * (dot * rso * rsv);
-      float dg = dG + through;
-      if (!p.has_h0 && c == 0 && tid == 0) dg = 0.0f;   // the first token's decay meets no state: exactly zero
+      float dgt = static_cast<float>(dg + static_cast<double>(before - z) + static_cast<double>(s.e[kC - 1] * (dot * rs1 * rs2)));
+      if (!p.has_h0 && c == 0 && tid == 0) dgt = 0.0f;   // the first token's decay meets no state: exactly zero
       float pa = 0.0f, pb = 0.0f;
       if (tid < left) {
         const int64_t i = (b * d.T + t0 + tid) * d.H + h;
         const float rate = exp2_fast(p.a_log[h] * kLog2e), z2 = p.a_raw[i] + p.dt_bias[h];
-        const float da = -rate * mscan::sigmoid(z2) * dg;
+        const float da = -rate * mscan::sigmoid(z2) * dgt;
         p.d_a_raw[i] = da;
         p.d_b_raw[i] = s.db[tid];
-        pa = -rate * mscan::softplus(z2) * dg;
+        pa = -rate * mscan::softplus(z2) * dgt;
         pb = da;
       }
       pa = wave_sum(pa);
@@ -651,7 +675,7 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) gdelta_bwd_chunk_kernel(c
         p.part[ci * 2 + 1] = pb;
       }
     }
-    __syncthreads();   // M, rows and the scalars are read
+    __syncthreads();   // M, its padding and the scalars are read
   }
   // unit length's adjoint: r (d - n (n . d))
 #pragma unroll
@@ -661,20 +685,12 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) gdelta_bwd_chunk_kernel(c
       float wq = 0.0f, wk = 0.0f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float kv = static_cast<float>(kt[0][n][mt >> 1][(mt & 1) * 4 + e]), qv = static_cast<float>(qt[0][n][mt >> 1][(mt & 1) * 4 + e]);
-        if (NP == 2) {
-          kv += static_cast<float>(kt[NP - 1][n][mt >> 1][(mt & 1) * 4 + e]);
-          qv += static_cast<float>(qt[NP - 1][n][mt >> 1][(mt & 1) * 4 + e]);
-        }
-        wq = fmaf(totQ[mt][n][e], qv, wq);
-        wk = fmaf(totK[mt][n][e], kv, wk);
+        wq = elem(qt[n], mt, e, totQ[mt][n][e], wq);
+        wk = elem(kt[n], mt, e, totK[mt][n][e], wk);
       }
       wq = sum16(wq);
       wk = sum16(wk);
-      if (r == 0) {
-        s.rows[wv][0][16 * mt + 4 * g + e] = wq;
-        s.rows[wv][1][16 * mt + 4 * g + e] = wk;
-      }
+      if (r == 0) s.pad(wv, 16 * mt + 4 * g + e) = f32x4{wq, wk, 0.0f, 0.0f};
     }
   __syncthreads();
   const float rscale = 1.0f / d.scale;
@@ -686,21 +702,21 @@ __global__ void __launch_bounds__(256, SHARED ? 1 : 2) gdelta_bwd_chunk_kernel(c
       const int i = 16 * mt + 4 * g + e;
       if (i >= left) continue;
       const float pq = gsc[G_PQ * kC + i], rq = s.rq[i], pk = gsc[G_PK * kC + i], rk = s.rk[i];
+      float wq = 0.0f, wk = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const f32x4 v = s.pad(w, i);
+        wq += v[0];
+        wk += v[1];
+      }
       const float un = rq * rscale;
-      const float wq = ((s.rows[0][0][i] + s.rows[1][0][i]) + (s.rows[2][0][i] + s.rows[3][0][i])) * un * un;
-      const float wk = ((s.rows[0][1][i] + s.rows[1][1][i]) + (s.rows[2][1][i] + s.rows[3][1][i])) * rk * rk;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int col = 16 * (n0 + n) + r;
+        const int col = 16 * (NT * wv + n) + r;
         if (col >= d.K) continue;
-        float kv = static_cast<float>(kt[0][n][mt >> 1][(mt & 1) * 4 + e]), qv = static_cast<float>(qt[0][n][mt >> 1][(mt & 1) * 4 + e]);
-        if (NP == 2) {
-          kv += static_cast<float>(kt[NP - 1][n][mt >> 1][(mt & 1) * 4 + e]);
-          qv += static_cast<float>(qt[NP - 1][n][mt >> 1][(mt & 1) * 4 + e]);
-        }
         const int64_t o = qk + i * (d.G * d.K) + col;
-        IO<A>::st(p.d_q, o, rq * (totQ[mt][n][e] - qv * wq) * pq);
-        IO<A>::st(p.d_k, o, rk * (totK[mt][n][e] - kv * wk) * pk);
+        IO<A>::st(p.d_q, o, rq * elem(qt[n], mt, e, -wq * un * un, totQ[mt][n][e]) * pq);
+        IO<A>::st(p.d_k, o, rk * elem(kt[n], mt, e, -wk * rk * rk, totK[mt][n][e]) * pk);
       }
     }
   }

@@ -703,17 +703,10 @@ __global__ void __launch_bounds__(512) gdelta_fwd_ring_kernel(const FwdArgs p) {
 // Eight lanes share R rows of the state (16-byte pieces of 128-byte lines), all in registers over the call's tokens;
 // both products of a token, S k and S q, are taken of the state before it: y = alpha S q + u (k . q).  Bound by
 // reading and writing the state once.
-__device__ __forceinline__ float sum8(float v) {   // over aligned groups of eight lanes
-  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xB1, 0xf, 0xf, true));    // lane ^ 1
-  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4E, 0xf, 0xf, true));    // lane ^ 2
-  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x141, 0xf, 0xf, true));   // 7 - lane
-  return v;
-}
-
 __device__ __forceinline__ float max8(float v) {
-  v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xB1, 0xf, 0xf, true)));
-  v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4E, 0xf, 0xf, true)));
-  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x141, 0xf, 0xf, true)));
+  v = fmaxf(v, dpp<0xB1>(v));
+  v = fmaxf(v, dpp<0x4E>(v));
+  return fmaxf(v, dpp<0x141>(v));
 }
 
 template <Act A>
