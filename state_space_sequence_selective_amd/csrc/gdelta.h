@@ -25,6 +25,8 @@
 // |ds_{t-1}| <= alpha_t (|ds_t| + scale max |dy|).
 #pragma once
 
+#include <type_traits>
+
 #include "scan_common.h"
 
 namespace gdelta {
@@ -42,6 +44,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kC = 64;          // tokens per chunk
 constexpr int kFrag = 512;      // u16 of one operand fragment: 64 lanes x 8
+constexpr int kRingTiles = 4;   // 16-column tiles of a workgroup that shares its fragments in LDS
 
 // per-token scalars of a chunk, per query / key head: k' = k pk is what the products take, k' rk the unit-length key;
 // q' = q pq, and q' rq the unit-length query times the scale
@@ -329,6 +332,36 @@ __device__ __forceinline__ void xcd_head(uint32_t n, uint32_t per, uint32_t head
     idx = n % per;
   }
 }
+
+template <Act A>
+struct PassPlace {   // where a wave's columns are
+  using Raw = std::conditional_t<A == Act::F32, uint32_t, uint16_t>;
+  static constexpr int ES = sizeof(Raw);
+  int lane, r, g, col, row;   // row: bytes from token to token
+  bool ok;
+  int64_t bh, h, b, bg, nc, T, HV;
+
+  // `tiles` 16-column tiles to a workgroup, of which this wave has number `tile`
+  __device__ __forceinline__ explicit PassPlace(const Dims& d, int tiles = 1, int tile = 0) {
+    lane = threadIdx.x & 63;
+    r = lane & 15;
+    g = lane >> 4;
+    uint32_t head, cb;
+    xcd_head(blockIdx.x, (d.VP / 16 + tiles - 1) / tiles, static_cast<uint32_t>(d.B * d.H), head, cb);
+    const uint32_t H = static_cast<uint32_t>(d.H), G = static_cast<uint32_t>(d.G);
+    bh = head;
+    h = head % H;
+    b = head / H;
+    bg = b * G + (head % H) / (H / G);
+    col = (cb * tiles + tile) * 16 + r;
+    ok = col < d.V;
+    row = static_cast<int>(d.H) * d.V * ES;
+    nc = d.nc;
+    T = d.T;
+    HV = h * d.V * ES;
+  }
+  __device__ __forceinline__ int64_t at_chunk(int64_t c) const { return (b * T + c * kC) * row + HV; }
+};
 
 // A wave's 16 columns of a chunk's [64][d_v] rows as raw bits: elements of rows 16 mt + 4 g + e.  Rows behind the sequence
 // repeat its last one (what they hold meets zeros).  base: the chunk's first row of the head; row: bytes from token to

@@ -13,8 +13,6 @@
 //   E_ij = dP_ij P_ij + dA_ij A_ij (j < i)
 //   dG_i = sum_j E_ij - sum_j E_ji + q_i.(e dO S^T)_i - k_i.(e beta Y S^T)_i - k_i.(.. U dS'^T)_i
 //   dg_t = sum_{i >= t} dG_i + sum_i k_i.(.. U dS'^T)_i + e_63 <dS', S>
-#include <type_traits>
-
 #include "gdelta_launch.h"
 
 namespace gdelta {
@@ -65,179 +63,218 @@ __global__ void __launch_bounds__(64) gdelta_dscale_kernel(const BwdArgs p) {
 }
 
 // ------------------------------------------------------------------ pass from the last chunk to the first
-// As the forward's pass: a wave holds 16 columns of dS^T and needs nothing of any other.
-template <Act A, int KP>
-__global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
-  constexpr int NP = A == Act::F32 ? 2 : 1, MT = KP / 16, KS = KP / 32, NF = KP / 8;
-  constexpr bool AHEAD = NP == 1;
-  using Raw = std::conditional_t<A == Act::F32, uint32_t, uint16_t>;
-  constexpr int ES = sizeof(Raw);
-  __shared__ __attribute__((aligned(16))) float s[4][kC];   // beta; beta e rk; exp(G_63 - G) rk; e rq
-  const Dims& d = p.d;
-  const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
-  uint32_t head, cb;
-  xcd_head(blockIdx.x, d.VP / 16, static_cast<uint32_t>(d.B * d.H), head, cb);
-  const uint32_t H = static_cast<uint32_t>(d.H), G = static_cast<uint32_t>(d.G);
-  const int64_t bh = head, h = head % H, b = head / H, bg = b * G + (head % H) / (H / G);
-  const int col = cb * 16 + r;
-  const bool ok = col < d.V;
-  const int vrow = static_cast<int>(d.H) * d.V * ES, vcol = (ok ? col : d.V - 1) * ES;
-  const int poff = (4 * g * d.VP + col) * 4;
-  const float so = p.so[bh], rso = 1.0f / so, rps = 1.0f / d.pscale, soc = ok ? so : 0.0f;
-  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+// As the forward's pass: a wave holds 16 columns of dS^T and needs nothing of any other, but for the fragments that the
+// tiles of a head share; they come a chunk ahead, to registers, or with many tiles to LDS.  Fragments of a chunk in the
+// shared buffer, in this order (16-bit inputs only):
+template <int KP>
+struct BwdRing {
+  static constexpr int NF = KP / 8, KF = 0, PT = NF, TT = PT + 12, QT = TT + 12, KT = QT + NF, N = KT + NF;
+};
+
+template <Act A, int KP, bool RING>
+struct BackChain {
+  static constexpr int NP = A == Act::F32 ? 2 : 1, MT = KP / 16, KS = KP / 32, NF = KP / 8;
+  using Place = PassPlace<A>;
+  using R = BwdRing<KP>;
   f32x4 dS[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) dS[mt] = zero;
-  h8 kf[NF], kt[NF], qt[NF], ph[6], pl[6], th[6], tl[6];
+  h8 kf[RING ? 1 : NF], kt[RING ? 1 : NF], qt[RING ? 1 : NF], ph[RING ? 1 : 6], pl[RING ? 1 : 6], th[RING ? 1 : 6], tl[RING ? 1 : 6];
   float sc[4], el;
   uint32_t v[4][4];
-  auto KFp = [&](int64_t c) { return p.w.KF + (bg * d.nc + c) * (NP * NF * kFrag); };
-  auto KTp = [&](int64_t c) { return p.w.KT + (bg * d.nc + c) * (NP * NF * kFrag); };
-  auto QTp = [&](int64_t c) { return p.w.QT + (bg * d.nc + c) * (NP * NF * kFrag); };
-  auto load_p = [&](int64_t c) {
-    const uint16_t* x = p.w.PT + (bh * d.nc + c) * (12 * kFrag);
-    load_frags(ph, x, lane);
-    load_frags(pl, x + 6 * kFrag, lane);
-  };
-  auto load_t = [&](int64_t c) {
-    const uint16_t* x = p.w.TT + (bh * d.nc + c) * (12 * kFrag);
-    load_frags(th, x, lane);
-    load_frags(tl, x + 6 * kFrag, lane);
-  };
-  auto load_sc = [&](int64_t c) {
-    const float* x = p.w.hsc + (bh * d.nc + c) * (kHeadSc * kC);
-    sc[0] = x[H_BETA * kC + lane];
-    sc[1] = x[H_BK * kC + lane];
-    sc[2] = x[H_DK * kC + lane];
-    sc[3] = x[H_EQ * kC + lane];
-    el = x[H_E * kC + kC - 1];
-  };
-  auto load_v = [&](int64_t c) {
-    load_cols<Raw>(v, static_cast<const char*>(p.dy) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES), vrow, vcol, d.T - c * kC, g);
-  };
-  if (AHEAD) {
-    load_frags(kf, KFp(d.nc - 1), lane);
-    load_p(d.nc - 1);
-    load_t(d.nc - 1);
-    load_frags(kt, KTp(d.nc - 1), lane);
-    load_frags(qt, QTp(d.nc - 1), lane);
+  const uint16_t* ring;   // + this lane's place
+
+  template <int N>
+  __device__ __forceinline__ h8 get(const h8 (&x)[N], int base, int i) const {
+    if constexpr (RING) return ld8(ring + (base + i) * kFrag);
+    else return x[i];
   }
-  load_sc(d.nc - 1);
-  load_v(d.nc - 1);
-  for (int64_t c = d.nc - 1; c >= 0; --c) {
-    const int64_t left = d.T - c * kC, ci = bh * d.nc + c;
-    const bool more = AHEAD && c > 0;
+  template <int N>
+  __device__ __forceinline__ void load(h8 (&x)[N], const uint16_t* base, int lane) {
+    if constexpr (!RING) load_frags(x, base, lane);
+  }
+  __device__ __forceinline__ int64_t group(const Place& w, int64_t c) const { return (w.bg * w.nc + c) * (NP * NF * kFrag); }
+  __device__ __forceinline__ void load_p(const BwdArgs& p, const Place& w, int64_t c) {
+    const uint16_t* x = p.w.PT + (w.bh * w.nc + c) * (12 * kFrag);
+    load(ph, x, w.lane);
+    load(pl, x + 6 * kFrag, w.lane);
+  }
+  __device__ __forceinline__ void load_t(const BwdArgs& p, const Place& w, int64_t c) {
+    const uint16_t* x = p.w.TT + (w.bh * w.nc + c) * (12 * kFrag);
+    load(th, x, w.lane);
+    load(tl, x + 6 * kFrag, w.lane);
+  }
+  __device__ __forceinline__ void load_sc(const BwdArgs& p, const Place& w, int64_t c) {
+    const float* x = p.w.hsc + (w.bh * w.nc + c) * (kHeadSc * kC);
+    sc[0] = x[H_BETA * kC + w.lane];
+    sc[1] = x[H_BK * kC + w.lane];
+    sc[2] = x[H_DK * kC + w.lane];
+    sc[3] = x[H_EQ * kC + w.lane];
+    el = x[H_E * kC + kC - 1];
+  }
+  __device__ __forceinline__ void load_dy(const BwdArgs& p, const Place& w, int64_t c) {
+    const int vcol = w.ok ? w.col : static_cast<int>(p.d.V) - 1;
+    load_cols<typename Place::Raw>(v, static_cast<const char*>(p.dy) + w.at_chunk(c), w.row, vcol * Place::ES, w.T - c * kC, w.g);
+  }
+  __device__ __forceinline__ void init(const BwdArgs& p, const Place& w) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t c = w.nc - 1;
+    load(kf, p.w.KF + group(w, c), w.lane);
+    load_sc(p, w, c);
+    load_dy(p, w, c);
+    load_p(p, w, c);
+    load_t(p, w, c);
+    load(qt, p.w.QT + group(w, c), w.lane);
+    load(kt, p.w.KT + group(w, c), w.lane);
+  }
+  // One chunk.  soc: the head's scale, 0 in columns behind d_v; s: [4][64] floats of the wave.
+  __device__ __forceinline__ void step(const BwdArgs& p, const Place& w, int64_t c, float soc, float rso, float rps, float (*s)[kC]) {
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t ci = w.bh * w.nc + c, next = c > 0 ? c - 1 : c;   // the first chunk loads its own again: no branch in the loop
+    const int VP = p.d.VP, poff = (4 * w.g * VP + w.col) * 4;
+    const uint16_t *KF = p.w.KF, *KT = p.w.KT, *QT = p.w.QT;
     mscan::wave_lds_sync();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i][lane] = sc[i];
+    for (int i = 0; i < 4; ++i) s[i][w.lane] = sc[i];
     mscan::wave_lds_sync();
     const float elc = el;
-    if (c > 0) load_sc(c - 1);
-    if (!AHEAD) {
-      load_frags(kf, KFp(c), lane);
-      load_p(c);
-    }
+    load_sc(p, w, next);
     f32x4 dU[4] = {zero, zero, zero, zero}, pd[4] = {zero, zero, zero, zero}, dO[4];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const Frag f = to_b(dS[2 * ks], dS[2 * ks + 1]);
-      store_packed(p.DS + (ci * KP + 32 * ks) * d.VP, poff, f, d.VP);
+      store_packed(p.DS + (ci * KP + 32 * ks) * VP, poff, f, VP);
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(kf[mt * KS + ks], f.hi, dU[mt]);
+      for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(get(kf, R::KF, mt * KS + ks), f.hi, dU[mt]);
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(kf[mt * KS + ks], f.lo, dU[mt]);
+      for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(get(kf, R::KF, mt * KS + ks), f.lo, dU[mt]);
       if (NP == 2) {
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(at<h8>(KFp(c) + (NF + mt * KS + ks) * kFrag, lane * 16), f.hi, dU[mt]);
+        for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(at<h8>(KF + group(w, c) + (NF + mt * KS + ks) * kFrag, w.lane * 16), f.hi, dU[mt]);
       }
     }
-    if (more) load_frags(kf, KFp(c - 1), lane);
+    load(kf, KF + group(w, next), w.lane);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) dO[mt][e] = IO<A>::cvt(v[mt][e]) * soc;
-    if (c > 0) load_v(c - 1);
+    load_dy(p, w, next);
     const Frag o0 = to_b(dO[0], dO[1]), o1 = to_b(dO[2], dO[3]);   // 16-bit input: the low parts are zero
 #pragma unroll
-    for (int f = 0; f < 6; ++f) pd[kUm[f]] = mma(ph[f], (kUk[f] ? o1 : o0).hi, pd[kUm[f]]);
+    for (int f = 0; f < 6; ++f) pd[kUm[f]] = mma(get(ph, R::PT, f), (kUk[f] ? o1 : o0).hi, pd[kUm[f]]);
 #pragma unroll
-    for (int f = 0; f < 6; ++f) pd[kUm[f]] = mma(pl[f], (kUk[f] ? o1 : o0).hi, pd[kUm[f]]);
+    for (int f = 0; f < 6; ++f) pd[kUm[f]] = mma(get(pl, R::PT + 6, f), (kUk[f] ? o1 : o0).hi, pd[kUm[f]]);
     if (NP == 2) {
 #pragma unroll
-      for (int f = 0; f < 6; ++f) pd[kUm[f]] = mma(ph[f], (kUk[f] ? o1 : o0).lo, pd[kUm[f]]);
+      for (int f = 0; f < 6; ++f) pd[kUm[f]] = mma(get(ph, R::PT, f), (kUk[f] ? o1 : o0).lo, pd[kUm[f]]);
     }
-    if (more) load_p(c - 1);
-    if (!AHEAD) {
-      load_t(c);
-      load_frags(kt, KTp(c), lane);
-      load_frags(qt, QTp(c), lane);
-    }
+    load_p(p, w, next);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      const f32x4 dk = *reinterpret_cast<const f32x4*>(s[2] + 16 * mt + 4 * g), eq = *reinterpret_cast<const f32x4*>(s[3] + 16 * mt + 4 * g);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        dU[mt][e] = fmaf(dU[mt][e], dk[e], pd[mt][e] * rps);
-        dO[mt][e] *= eq[e];
-      }
+      const f32x4 dk = *reinterpret_cast<const f32x4*>(s[2] + 16 * mt + 4 * w.g);
+      dU[mt] = dU[mt] * dk + pd[mt] * rps;
+      dO[mt] *= *reinterpret_cast<const f32x4*>(s[3] + 16 * mt + 4 * w.g);
     }
     const Frag u0 = to_b(dU[0], dU[1]), u1 = to_b(dU[2], dU[3]);
     f32x4 Y[4] = {zero, zero, zero, zero};
 #pragma unroll
-    for (int f = 0; f < 6; ++f) Y[kUm[f]] = mma(th[f], (kUk[f] ? u1 : u0).hi, Y[kUm[f]]);
+    for (int f = 0; f < 6; ++f) Y[kUm[f]] = mma(get(th, R::TT, f), (kUk[f] ? u1 : u0).hi, Y[kUm[f]]);
 #pragma unroll
-    for (int f = 0; f < 6; ++f) Y[kUm[f]] = mma(th[f], (kUk[f] ? u1 : u0).lo, Y[kUm[f]]);
+    for (int f = 0; f < 6; ++f) Y[kUm[f]] = mma(get(th, R::TT, f), (kUk[f] ? u1 : u0).lo, Y[kUm[f]]);
 #pragma unroll
-    for (int f = 0; f < 6; ++f) Y[kUm[f]] = mma(tl[f], (kUk[f] ? u1 : u0).hi, Y[kUm[f]]);
-    if (more) load_t(c - 1);
-    // e0, e1 and the state's part of dS from dO do not wait for Y
+    for (int f = 0; f < 6; ++f) Y[kUm[f]] = mma(get(tl, R::TT + 6, f), (kUk[f] ? u1 : u0).hi, Y[kUm[f]]);
+    load_t(p, w, next);
+    // the part of dS from dO does not wait for Y
     const Frag e0 = to_b(dO[0], dO[1]), e1 = to_b(dO[2], dO[3]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dS[mt][e] *= elc;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(qt[2 * mt], e0.hi, dS[mt]);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(qt[2 * mt], e0.lo, dS[mt]);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(qt[2 * mt + 1], e1.hi, dS[mt]);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(qt[2 * mt + 1], e1.lo, dS[mt]);
-    if (NP == 2) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        dS[mt] = mma(at<h8>(QTp(c) + (NF + 2 * mt) * kFrag, lane * 16), e0.hi, dS[mt]);
-        dS[mt] = mma(at<h8>(QTp(c) + (NF + 2 * mt + 1) * kFrag, lane * 16), e1.hi, dS[mt]);
-      }
-    }
-    if (more) load_frags(qt, QTp(c - 1), lane);
-    store_packed(p.DU + ci * kC * d.VP, poff, to_b(Y[0], Y[1]), d.VP);
-    store_packed(p.DU + (ci * kC + 32) * d.VP, poff, to_b(Y[2], Y[3]), d.VP);
+    for (int mt = 0; mt < MT; ++mt) dS[mt] *= elc;
+    update(qt, R::QT, QT + group(w, c), e0, e1, w.lane);
+    load(qt, QT + group(w, next), w.lane);
+    store_packed(p.DU + ci * kC * VP, poff, to_b(Y[0], Y[1]), VP);
+    store_packed(p.DU + (ci * kC + 32) * VP, poff, to_b(Y[2], Y[3]), VP);
     f32x4 dv[4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      dv[mt] = Y[mt] * *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * g) * rso;
-      Y[mt] *= -*reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * g);
+      dv[mt] = Y[mt] * *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * w.g) * rso;
+      Y[mt] *= -*reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * w.g);
     }
-    store_cols<A>(dv, static_cast<char*>(p.d_v) + ((b * d.T + c * kC) * d.H + h) * (d.V * ES), vrow, col * ES, left, g, ok);
-    const Frag y0 = to_b(Y[0], Y[1]), y1 = to_b(Y[2], Y[3]);
+    update(kt, R::KT, KT + group(w, c), to_b(Y[0], Y[1]), to_b(Y[2], Y[3]), w.lane);
+    load(kt, KT + group(w, next), w.lane);
+    store_cols<A>(dv, static_cast<char*>(p.d_v) + w.at_chunk(c), w.row, w.col * Place::ES, w.T - c * kC, w.g, w.ok);
+  }
+  // dS += X^T (a, b): X's transposed fragments; f32 inputs have a second plane in global memory
+  template <int N>
+  __device__ __forceinline__ void update(const h8 (&x)[N], int base, const uint16_t* global, const Frag& a, const Frag& b, int lane) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(kt[2 * mt], y0.hi, dS[mt]);
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get(x, base, 2 * mt), a.hi, dS[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(kt[2 * mt], y0.lo, dS[mt]);
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get(x, base, 2 * mt), a.lo, dS[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(kt[2 * mt + 1], y1.hi, dS[mt]);
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get(x, base, 2 * mt + 1), b.hi, dS[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(kt[2 * mt + 1], y1.lo, dS[mt]);
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get(x, base, 2 * mt + 1), b.lo, dS[mt]);
     if (NP == 2) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        dS[mt] = mma(at<h8>(KTp(c) + (NF + 2 * mt) * kFrag, lane * 16), y0.hi, dS[mt]);
-        dS[mt] = mma(at<h8>(KTp(c) + (NF + 2 * mt + 1) * kFrag, lane * 16), y1.hi, dS[mt]);
+        dS[mt] = mma(at<h8>(global + (NF + 2 * mt) * kFrag, lane * 16), a.hi, dS[mt]);
+        dS[mt] = mma(at<h8>(global + (NF + 2 * mt + 1) * kFrag, lane * 16), b.hi, dS[mt]);
       }
     }
-    if (more) load_frags(kt, KTp(c - 1), lane);
+  }
+};
+
+template <Act A, int KP>
+__global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
+  __shared__ __attribute__((aligned(16))) float s[4][kC];   // beta; beta e rk; exp(G_63 - G) rk; e rq
+  const PassPlace<A> w(p.d);
+  const float so = p.so[w.bh], rso = 1.0f / so, rps = 1.0f / p.d.pscale, soc = w.ok ? so : 0.0f;
+  BackChain<A, KP, false> ch;
+  ch.init(p, w);
+  for (int64_t c = p.d.nc - 1; c >= 0; --c) ch.step(p, w, c, soc, rso, rps, s);
+}
+
+// Four waves with a tile each and four that copy the fragments, as in the forward
+template <Act A, int KP>
+__global__ void __launch_bounds__(512) gdelta_bwd_ring_kernel(const BwdArgs p) {
+  using R = BwdRing<KP>;
+  constexpr int NF = R::NF;
+  __shared__ __attribute__((aligned(16))) uint16_t ring[2][R::N * kFrag];
+  __shared__ __attribute__((aligned(16))) float s[kRingTiles][4][kC];
+  static_assert(sizeof(ring) + sizeof(s) <= mscan::kLdsBytes, "LDS");
+  const Dims& d = p.d;
+  const int wv = wave_id();
+  const PassPlace<A> w(d, kRingTiles, wv & (kRingTiles - 1));
+  const int64_t last = d.nc - 1;
+  if (wv >= kRingTiles) {
+    const int first = wv - kRingTiles;
+    auto copy = [&](int64_t c) {
+      uint16_t* dst = ring[c & 1];
+      const int64_t gi = (w.bg * d.nc + c) * (NF * kFrag), ci = (w.bh * d.nc + c) * (12 * kFrag);
+      copy_frags<NF, kRingTiles>(dst + R::KF * kFrag, p.w.KF + gi, first, w.lane);
+      copy_frags<12, kRingTiles>(dst + R::PT * kFrag, p.w.PT + ci, first, w.lane);
+      copy_frags<12, kRingTiles>(dst + R::TT * kFrag, p.w.TT + ci, first, w.lane);
+      copy_frags<NF, kRingTiles>(dst + R::QT * kFrag, p.w.QT + gi, first, w.lane);
+      copy_frags<NF, kRingTiles>(dst + R::KT * kFrag, p.w.KT + gi, first, w.lane);
+      wait_copies();
+    };
+    copy(last);
+    mscan::lds_barrier();
+    for (int64_t c = last; c >= 0; --c) {
+      if (c > 0) copy(c - 1);
+      mscan::lds_barrier();   // chunk c - 1 is there, and chunk c's readers are done
+    }
+    return;
+  }
+  const float so = p.so[w.bh], rso = 1.0f / so, rps = 1.0f / d.pscale, soc = w.ok ? so : 0.0f;
+  const bool live = w.col < d.VP;   // a head's last workgroup may have tiles behind its columns
+  BackChain<A, KP, true> ch;
+  if (live) ch.init(p, w);
+  mscan::lds_barrier();
+  for (int64_t c = last; c >= 0; --c) {
+    if (live) {
+      ch.ring = ring[c & 1] + w.lane * 8;
+      ch.step(p, w, c, soc, rso, rps, s[wv]);
+    }
+    mscan::lds_barrier();
   }
 }
 
@@ -759,7 +796,12 @@ hipError_t launch(const BwdArgs& a, hipStream_t st) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(gdelta_dscale_kernel, dim3(bh), dim3(64), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL((gdelta_bwd_state_kernel<A, KP>), dim3(bh * (d.VP / 16)), dim3(64), 0, st, a);
+  const unsigned tiles = d.VP / 16;
+  if (A == Act::F32 || bh * tiles <= kPairTiles) {
+    hipLaunchKernelGGL((gdelta_bwd_state_kernel<A, KP>), dim3(bh * tiles), dim3(64), 0, st, a);
+  } else if constexpr (A != Act::F32) {
+    hipLaunchKernelGGL((gdelta_bwd_ring_kernel<A, KP>), dim3(bh * ((tiles + kRingTiles - 1) / kRingTiles)), dim3(512), 0, st, a);
+  }
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const dim3 grid(static_cast<unsigned>(d.B * d.G) * nc);
   if (d.H == d.G) hipLaunchKernelGGL((gdelta_bwd_chunk_kernel<A, KP, false>), grid, dim3(256), 0, st, a);

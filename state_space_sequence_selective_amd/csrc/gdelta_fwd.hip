@@ -1,8 +1,6 @@
 // Gated delta rule, forward: the chunks' operands, the per-chunk triangular
 // inverse, the pass over the chunks, and the token-by-token step (gfx950).
 // The algebra and the number format are in gdelta.h.
-#include <type_traits>
-
 #include "gdelta_launch.h"
 
 namespace gdelta {
@@ -325,36 +323,6 @@ struct PassBuf {
   h8 S[KP / 32][2][64], U[2][2][64];   // [step][high, low][lane]
 };
 
-template <Act A>
-struct PassPlace {   // where a wave's columns are
-  using Raw = std::conditional_t<A == Act::F32, uint32_t, uint16_t>;
-  static constexpr int ES = sizeof(Raw);
-  int lane, r, g, col, row;   // row: bytes from token to token
-  bool ok;
-  int64_t bh, h, b, bg, nc, T, HV;
-
-  // `tiles` 16-column tiles to a workgroup, of which this wave has number `tile`
-  __device__ __forceinline__ explicit PassPlace(const Dims& d, int tiles = 1, int tile = 0) {
-    lane = threadIdx.x & 63;
-    r = lane & 15;
-    g = lane >> 4;
-    uint32_t head, cb;
-    xcd_head(blockIdx.x, (d.VP / 16 + tiles - 1) / tiles, static_cast<uint32_t>(d.B * d.H), head, cb);
-    const uint32_t H = static_cast<uint32_t>(d.H), G = static_cast<uint32_t>(d.G);
-    bh = head;
-    h = head % H;
-    b = head / H;
-    bg = b * G + (head % H) / (H / G);
-    col = (cb * tiles + tile) * 16 + r;
-    ok = col < d.V;
-    row = static_cast<int>(d.H) * d.V * ES;
-    nc = d.nc;
-    T = d.T;
-    HV = h * d.V * ES;
-  }
-  __device__ __forceinline__ int64_t at_chunk(int64_t c) const { return (b * T + c * kC) * row + HV; }
-};
-
 // Fragments of a chunk in a shared buffer, in this order; 16-bit inputs only
 template <Act A, int KP>
 struct FwdRing {
@@ -644,8 +612,6 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
 // The same for many tiles: four waves with a tile of one head each, and four that copy the chunk's fragments into LDS
 // (66 KB for d_k = 128 and bf16, twice) a chunk ahead.  A CU takes about 12 bytes a clock from L2 here, so what bounds
 // the kernel above, once it has several waves a CU, is every wave loading its own copy.
-constexpr int kRingTiles = 4;
-
 template <Act A, int KP, bool SAVE>
 __global__ void __launch_bounds__(512) gdelta_fwd_ring_kernel(const FwdArgs p) {
   using R = FwdRing<A, KP>;
