@@ -25,13 +25,17 @@ __global__ void __launch_bounds__(256) gdelta_dymax_kernel(const BwdArgs p) {
   const int tid = threadIdx.x;
   const int64_t c = blockIdx.x % d.nc, bh = blockIdx.x / d.nc, h = bh % d.H, b = bh / d.H;
   const int64_t t0 = c * kC, left = d.T - t0;
-  const int nv = d.V / 8, rows = left < kC ? static_cast<int>(left) : kC;
   float m = 0.0f;
-  for (int i = tid; i < rows * nv; i += 256) {
-    float x[8];
-    load8<A>(p.dy, ((b * d.T + t0 + i / nv) * d.H + h) * d.V + (i % nv) * 8, true, x);
+  const int row = tid >> 2;   // four threads a row, four loads in flight
+  for (int c0 = (tid & 3) * 8; c0 < d.V; c0 += 4 * 32) {
+    float x[4][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max_finite(m, x[e]);
+    for (int k = 0; k < 4; ++k)
+      load8<A>(p.dy, ((b * d.T + t0 + row) * d.H + h) * d.V + c0 + 32 * k, row < left && c0 + 32 * k < d.V, x[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max_finite(m, x[k][e]);
   }
   m = wave_max(m);
   if ((tid & 63) == 0) s[tid >> 6] = m;
@@ -296,7 +300,7 @@ struct ChunkLds {
     uint16_t M[8][kC * kCol];   // high and low parts of M1, its transpose, M2, its transpose
   };
   double G[kC], rowE[10][16], colE[10][16];   // E's sums, by lower tile
-  float beta[kC], e[kC], dec[kC], rk[kC], rq[kC], db[kC];
+  float beta[kC], e[kC], dec[kC], rk[kC], rq[kC], pk[kC], pq[kC], db[kC];
   float red[2][8];
 
   // four floats in the padding of row i of plane n: the waves' row sums
@@ -317,13 +321,14 @@ __device__ __forceinline__ int lower_row(int n) { return n < 1 ? 0 : n < 3 ? 1 :
 __device__ __forceinline__ int lower_col(int n) { return n - lower_row(n) * (lower_row(n) + 1) / 2; }
 
 template <Act A, int KP, bool SHARED>
-__global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs p) {
+__global__ void __launch_bounds__(256, SHARED && KP == 128 ? 1 : 2) gdelta_bwd_chunk_kernel(const BwdArgs p) {
   constexpr int NP = A == Act::F32 ? 2 : 1, KS = KP / 32, NF = KP / 8, NW = 4, NTHR = NW * 64, NT = KP / 64;   // NT tiles of 16 d_k rows to a wave
   constexpr int CPT = 64 * 32 / NTHR, SUB = CPT / 4, TILES = (10 + NW - 1) / NW;   // a thread's columns of a slab, in fours
   __shared__ __attribute__((aligned(16))) ChunkLds<A> s;
   static_assert(sizeof(s) <= mscan::kLdsBytes / 2, "two workgroups a CU");
   const Dims& d = p.d;
-  const int tid = threadIdx.x, lane = tid & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
+  int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int wv = wave_id();
   const uint32_t nc32 = static_cast<uint32_t>(d.nc), G32 = static_cast<uint32_t>(d.G);
   const int64_t c = blockIdx.x % nc32, bg = blockIdx.x / nc32, hk = bg % G32, b = static_cast<uint32_t>(bg) / G32;
   const int64_t t0 = c * kC, left = d.T - t0, gi = bg * d.nc + c;
@@ -346,7 +351,12 @@ __global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs 
   for (int hi_ = 0; hi_ < share; ++hi_) {
     const int64_t h = hk * share + hi_, bh = b * d.H + h, ci = bh * d.nc + c;
     int64_t fo = gi * (NP * NF * kFrag);
-    if (SHARED) asm volatile("" : "+s"(fo));   // or the heads' loop keeps every fragment of k and q in registers
+    if (SHARED) {   // or the heads' loop keeps every fragment of k and q, and every lane's addresses, in registers
+      asm volatile("" : "+s"(fo), "+v"(tid));
+      lane = tid & 63;
+      r = lane & 15;
+      g = lane >> 4;
+    }
     const uint16_t* KF = p.w.KF + fo;
     const uint16_t* QF = p.w.QF + fo;
     const uint16_t* KT = p.w.KT + fo;
@@ -409,7 +419,12 @@ __global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs 
       s.dec[tid] = exp2_fast(static_cast<float>(Gl - G));
       s.rk[tid] = gsc[G_RK * kC + tid];
       s.rq[tid] = gsc[G_RQ * kC + tid];
+      s.pk[tid] = gsc[G_PK * kC + tid];
+      s.pq[tid] = gsc[G_PQ * kC + tid];
     }
+    // what the decay's gradient reads at the end
+    const float rate = exp2_fast(p.a_log[h] * kLog2e), bias = p.dt_bias[h];
+    const float a_raw = tid < kC && tid < left ? p.a_raw[(b * d.T + t0 + tid) * d.H + h] : 0.0f;
     for (int v0 = 0; v0 < d.VP; v0 += 32) {
       auto& sl = s.slab[(v0 >> 5) & 1];
 #pragma unroll
@@ -484,8 +499,7 @@ __global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs 
       }
 #pragma unroll
       for (int i = 0; i < TILES; ++i) {   // lower tiles wv, wv + NW, ..
-        const int tl = wv + NW * i;
-        if (tl >= 10) break;
+        const int tl = min(wv + NW * i, 9);
         const int a = (16 * lower_row(tl) + r) * kSlab + 8 * g, bb = (16 * lower_col(tl) + r) * kSlab + 8 * g;
         const h8 oh = ld8(sl.dO[0] + a), yh = ld8(sl.Y[0] + a), yl = ld8(sl.Y[1] + a);
         const h8 uh = ld8(sl.U[0] + bb), ul = ld8(sl.U[1] + bb);
@@ -512,8 +526,8 @@ __global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs 
 #pragma unroll
     for (int i = 0; i < TILES; ++i) {
       m1[i] = m2[i] = zero;
-      const int tl = wv + NW * i;
-      if (tl >= 10) break;
+      const bool mine = wv + NW * i < 10;   // else the last tile again, for nothing: one path for all waves
+      const int tl = mine ? wv + NW * i : 9;
       const int mt = lower_row(tl), nt = lower_col(tl), j = 16 * nt + r, i0 = 16 * mt + 4 * g;
       const f32x4 kq = frag_mm<NP, KS, NF>(QF + mt * KS * kFrag, KF + nt * KS * kFrag, lane, zero);
       const f32x4 kk = frag_mm<NP, KS, NF>(KF + mt * KS * kFrag, KF + nt * KS * kFrag, lane, zero);
@@ -521,7 +535,8 @@ __global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs 
       const f32x4 be = *reinterpret_cast<const f32x4*>(s.beta + i0);
       const float rkj = s.rk[j];
       const double Gj = s.G[j];
-      double ce = 0.0;
+      float db = 0.0f;
+      double ce = 0.0, re[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int ti = i0 + e;
@@ -533,17 +548,23 @@ __global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs 
           m2[i][e] = -yu * be[e] * D;
           E = m1[i][e] * (rq[e] * rkj * kq[e]) + m2[i][e] * (rk[e] * rkj * kk[e]);
         }
-        if (ti == j) s.db[ti] = yu * (1.0f - be[e]);
+        db = ti == j ? yu * (1.0f - be[e]) : db;
         // the sums over rows and over columns cancel where a token's g stands between neither or both of a pair: in
         // f64 they do so to the last bit of E
         ce += static_cast<double>(E);
-        const double re = sum16(static_cast<double>(E));
-        if (r == 0) s.rowE[tl][4 * g + e] = re;
+        re[e] = sum16(static_cast<double>(E));
         big = max_finite(big, fmaxf(fabsf(m1[i][e]), fabsf(m2[i][e])) * fmaxf(rkj, fmaxf(fabsf(rq[e]), rk[e])));
       }
       ce += __shfl_xor(ce, 16, 64);
       ce += __shfl_xor(ce, 32, 64);
-      if (g == 0) s.colE[tl][r] = ce;
+      if (mine) {
+        if (r == 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s.rowE[tl][4 * g + e] = re[e];
+        }
+        if (g == 0) s.colE[tl][r] = ce;
+        if (mt == nt && r >> 2 == g) s.db[j] = db;
+      }
     }
     big = wave_max(big);
     dot = wave_sum(dot);
@@ -607,6 +628,7 @@ __global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs 
         aKq[mt][n] = aKq[mt][n] * (ev * be * -rs1) * rs2;
         aKs[mt][n] = aKs[mt][n] * (de * rs1) * rs2;
       }
+      f32x4 sums[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float wq = 0.0f, wkq = 0.0f, wks = 0.0f;
@@ -616,10 +638,11 @@ __global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs 
           wkq = elem(kt[n], mt, e, aKq[mt][n][e], wkq);
           wks = elem(kt[n], mt, e, aKs[mt][n][e], wks);
         }
-        wq = sum16(wq);
-        wkq = sum16(wkq);
-        wks = sum16(wks);
-        if (r == 0) s.pad(wv, i0 + e) = f32x4{wq, wkq, wks, 0.0f};
+        sums[e] = f32x4{sum16(wq), sum16(wkq), sum16(wks), 0.0f};
+      }
+      if (r == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s.pad(wv, i0 + e) = sums[e];
       }
     }
     mscan::lds_barrier();
@@ -698,7 +721,7 @@ __global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs 
       float pa = 0.0f, pb = 0.0f;
       if (tid < left) {
         const int64_t i = (b * d.T + t0 + tid) * d.H + h;
-        const float rate = exp2_fast(p.a_log[h] * kLog2e), z2 = p.a_raw[i] + p.dt_bias[h];
+        const float z2 = a_raw + bias;
         const float da = -rate * mscan::sigmoid(z2) * dgt;
         p.d_a_raw[i] = da;
         p.d_b_raw[i] = s.db[tid];
@@ -716,7 +739,8 @@ __global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs 
   }
   // unit length's adjoint: r (d - n (n . d))
 #pragma unroll
-  for (int mt = 0; mt < 4; ++mt)
+  for (int mt = 0; mt < 4; ++mt) {
+    f32x4 sums[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float wq = 0.0f, wk = 0.0f;
@@ -725,35 +749,39 @@ __global__ void __launch_bounds__(256, 2) gdelta_bwd_chunk_kernel(const BwdArgs 
         wq = elem(qt[n], mt, e, totQ[mt][n][e], wq);
         wk = elem(kt[n], mt, e, totK[mt][n][e], wk);
       }
-      wq = sum16(wq);
-      wk = sum16(wk);
-      if (r == 0) s.pad(wv, 16 * mt + 4 * g + e) = f32x4{wq, wk, 0.0f, 0.0f};
+      sums[e] = f32x4{sum16(wq), sum16(wk), 0.0f, 0.0f};
     }
+    if (r == 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s.pad(wv, 16 * mt + 4 * g + e) = sums[e];
+    }
+  }
   __syncthreads();
   const float rscale = 1.0f / d.scale;
   const int64_t qk = ((b * d.T + t0) * d.G + hk) * d.K;
+  const int row = static_cast<int>(d.G) * d.K;   // elements from token to token
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
+    const int i0 = 16 * mt + 4 * g;
+    const f32x4 pq = *reinterpret_cast<const f32x4*>(s.pq + i0), rq = *reinterpret_cast<const f32x4*>(s.rq + i0);
+    const f32x4 pk = *reinterpret_cast<const f32x4*>(s.pk + i0), rk = *reinterpret_cast<const f32x4*>(s.rk + i0);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int i = 16 * mt + 4 * g + e;
-      if (i >= left) continue;
-      const float pq = gsc[G_PQ * kC + i], rq = s.rq[i], pk = gsc[G_PK * kC + i], rk = s.rk[i];
-      float wq = 0.0f, wk = 0.0f;
+      f32x4 w = s.pad(0, i0 + e);
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const f32x4 v = s.pad(w, i);
-        wq += v[0];
-        wk += v[1];
-      }
-      const float un = rq * rscale;
+      for (int n = 1; n < NW; ++n) w += s.pad(n, i0 + e);
+      const float un = rq[e] * rscale, fq = -w[0] * un * un, fk = -w[1] * rk[e] * rk[e];
+      const bool in = i0 + e < left;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int col = 16 * (NT * wv + n) + r;
-        if (col >= d.K) continue;
-        const int64_t o = qk + i * (d.G * d.K) + col;
-        IO<A>::st(p.d_q, o, rq * elem(qt[n], mt, e, -wq * un * un, totQ[mt][n][e]) * pq);
-        IO<A>::st(p.d_k, o, rk * elem(kt[n], mt, e, -wk * rk * rk, totK[mt][n][e]) * pk);
+        const float vq = rq[e] * elem(qt[n], mt, e, fq, totQ[mt][n][e]) * pq[e];
+        const float vk = rk[e] * elem(kt[n], mt, e, fk, totK[mt][n][e]) * pk[e];
+        if (in && col < d.K) {
+          const int64_t o = qk + (i0 + e) * row + col;
+          IO<A>::st(p.d_q, o, vq);
+          IO<A>::st(p.d_k, o, vk);
+        }
       }
     }
   }

@@ -128,14 +128,34 @@ __device__ __forceinline__ f32x4 tile_mm(const float* a, f32x4 b, int r, int g, 
 template <Act A, int KP>
 __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
   constexpr int NP = A == Act::F32 ? 2 : 1, KS = KP / 32, NF = KP / 8;
-  __shared__ __attribute__((aligned(16))) float sA[kC * kAS], sT[kC * kAS];
+  __shared__ __attribute__((aligned(16))) float sA[kC * kAS];   // A, and block by block its place taken by T
   __shared__ double sG[kC];
-  __shared__ float sBeta[kC], sRk[kC], sRq[kC], sMax[4];
+  __shared__ __attribute__((aligned(16))) float sBeta[kC], sRk[kC], sRq[kC];
+  __shared__ float sMax[4];
   const Dims& d = p.d;
   const int tid = threadIdx.x, lane = tid & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
-  const int64_t c = blockIdx.x % d.nc, bh = blockIdx.x / d.nc, h = bh % d.H, b = bh / d.H, hk = h / (d.H / d.G);
+  const uint32_t nc32 = static_cast<uint32_t>(d.nc), H32 = static_cast<uint32_t>(d.H);
+  const uint32_t head = blockIdx.x / nc32;
+  const int64_t c = blockIdx.x % nc32, bh = head, h = head % H32, b = head / H32, hk = (head % H32) / (H32 / static_cast<uint32_t>(d.G));
   const int64_t t0 = c * kC, left = d.T - t0, ci = bh * d.nc + c, gi = (b * d.G + hk) * d.nc + c;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const uint16_t* KF = p.w.KF + gi * (NP * NF * kFrag);
+  const uint16_t* QF = p.w.QF + gi * (NP * NF * kFrag);
+  // Wave w's operands: k of tiles 0 .. w, q of tiles w .. 3 (five tiles), and k and q of tile w; all in flight while the
+  // gates are made.  A slot s <= w gives the tile (rows j of s, columns i of w) of k.k^T and k.q^T, a later one (rows i
+  // of s - 1, columns j of w) of q.k^T.
+  h8 x[5][KS], bk[KS], bq[KS];
+#pragma unroll
+  for (int s = 0; s < 5; ++s) {
+    const uint16_t* src = s <= wv ? KF + s * KS * kFrag : QF + (s - 1) * KS * kFrag;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) x[s][ks] = at<h8>(src + ks * kFrag, lane * 16);
+  }
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    bk[ks] = at<h8>(KF + (wv * KS + ks) * kFrag, lane * 16);
+    bq[ks] = at<h8>(QF + (wv * KS + ks) * kFrag, lane * 16);
+  }
   if (tid < kC) {
     const bool ok = tid < left;
     const int64_t i = (b * d.T + t0 + tid) * d.H + h;
@@ -143,12 +163,11 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
     double G = ok ? log2_decay(rate, p.a_raw[i], p.dt_bias[h]) : 0.0f;
     const float beta = ok ? mscan::sigmoid(p.b_raw[i]) : 0.0f;
     const float rk = p.w.gsc[gi * (kGroupSc * kC) + G_RK * kC + tid], rq = p.w.gsc[gi * (kGroupSc * kC) + G_RQ * kC + tid];
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const double o = __shfl_up(G, s, 64);
-      if (lane >= s) G += o;
-    }
-    const double Gl = __shfl(G, 63, 64);
+    G = wave_scan(G);
+    const uint64_t gb = __builtin_bit_cast(uint64_t, G);
+    const uint64_t glo = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(gb), 63));
+    const uint64_t ghi = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(gb >> 32), 63));
+    const double Gl = __builtin_bit_cast(double, (ghi << 32) | glo);
     sG[tid] = G;
     sBeta[tid] = beta;
     sRk[tid] = rk;
@@ -165,13 +184,16 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
   // the largest |v|, and the initial state's bound sqrt(d_k) max |h0|
   float m = 0.0f;
   {
-    const int nv = d.V / 8;
-    const int rows = left < kC ? static_cast<int>(left) : kC;
-    for (int i = tid; i < rows * nv; i += 256) {
-      float x[8];
-      load8<A>(p.v, ((b * d.T + t0 + i / nv) * d.H + h) * d.V + (i % nv) * 8, true, x);
+    const int row = tid >> 2;   // four threads a row, four loads in flight
+    for (int c0 = (tid & 3) * 8; c0 < d.V; c0 += 4 * 32) {
+      float y[4][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = max_finite(m, x[e]);
+      for (int k = 0; k < 4; ++k)
+        load8<A>(p.v, ((b * d.T + t0 + row) * d.H + h) * d.V + c0 + 32 * k, row < left && c0 + 32 * k < d.V, y[k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max_finite(m, y[k][e]);
     }
     if (c == 0 && p.h0) {
       float m0 = 0.0f;
@@ -183,29 +205,52 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
   }
   __syncthreads();
   if (tid == 0) p.w.vmax[ci] = fmaxf(fmaxf(sMax[0], sMax[1]), fmaxf(sMax[2], sMax[3]));
-  const uint16_t* KF = p.w.KF + gi * (NP * NF * kFrag);
-  const uint16_t* QF = p.w.QF + gi * (NP * NF * kFrag);
   {
-    // wave w: tiles (rows j of tile n, columns i of tile w), n <= w
     const int i = 16 * wv + r;
     const float rki = sRk[i], rqi = sRq[i], be = sBeta[i];
     const double Gi = sG[i];
-    f32x4 P[4];
+    f32x4 P[4], PT[4];   // tile n of this wave's row of P's transpose, and of P
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      P[n] = zero;
-      if (n > wv) continue;
-      const f32x4 kk = frag_mm<NP, KS, NF>(KF + n * KS * kFrag, KF + wv * KS * kFrag, lane, zero);
-      const f32x4 kq = frag_mm<NP, KS, NF>(KF + n * KS * kFrag, QF + wv * KS * kFrag, lane, zero);
-      f32x4 a;
+    for (int n = 0; n < 4; ++n) P[n] = PT[n] = zero;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = 16 * n + 4 * g + e;
-        const float w = j <= i ? sRk[j] * exp2_fast(static_cast<float>(Gi - sG[j])) : 0.0f;
-        P[n][e] = rqi * w * kq[e];
-        a[e] = j < i ? be * rki * w * kk[e] : 0.0f;
+    for (int s = 0; s < 5; ++s) {
+      f32x4 xk = zero, xq = zero;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        xk = mma(x[s][ks], bk[ks], xk);
+        xq = mma(x[s][ks], bq[ks], xq);
       }
-      *reinterpret_cast<f32x4*>(sA + i * kAS + 16 * n + 4 * g) = a;
+      if (NP == 2) {   // the planes of low parts
+        const uint16_t* src = s <= wv ? KF + s * KS * kFrag : QF + (s - 1) * KS * kFrag;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const h8 xl = at<h8>(src + (NF + ks) * kFrag, lane * 16);
+          xk = mma(xl, bk[ks], xk);
+          xq = mma(xl, bq[ks], xq);
+          xk = mma(x[s][ks], at<h8>(KF + (NF + wv * KS + ks) * kFrag, lane * 16), xk);
+          xq = mma(x[s][ks], at<h8>(QF + (NF + wv * KS + ks) * kFrag, lane * 16), xq);
+        }
+      }
+      if (s <= wv) {   // rows j, column i
+        const int j0 = 16 * s + 4 * g;
+        const f32x4 rkj = *reinterpret_cast<const f32x4*>(sRk + j0);
+        f32x4 a, q;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = j0 + e <= i ? rkj[e] * exp2_fast(static_cast<float>(Gi - sG[j0 + e])) : 0.0f;
+          q[e] = rqi * w * xq[e];
+          a[e] = j0 + e < i ? be * rki * w * xk[e] : 0.0f;
+        }
+        if (s < 4) P[s < 4 ? s : 3] = q;
+        *reinterpret_cast<f32x4*>(sA + i * kAS + j0) = a;
+      } else {         // rows i', column j = i
+        const int i0 = 16 * (s - 1) + 4 * g;
+        const f32x4 rq = *reinterpret_cast<const f32x4*>(sRq + i0);
+        f32x4 q;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] = i <= i0 + e ? rq[e] * rki * exp2_fast(static_cast<float>(sG[i0 + e] - Gi)) * xk[e] : 0.0f;
+        PT[s > 0 ? s - 1 : 0] = q;
+      }
     }
     constexpr int PP = kPPlanes<A>;
     uint16_t* dst = p.w.P + ci * (PP * 6 * kFrag);
@@ -213,100 +258,91 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
     for (int ks = 0; ks < 2; ++ks) {
       if (ks == 1 && wv < 2) continue;
       const int f = wv < 2 ? wv : 2 * wv - 2 + ks;
-      const Frag x = to_b(P[2 * ks], P[2 * ks + 1]);
-      at<h8>(dst + f * kFrag, lane * 16) = x.hi;
-      if (PP == 2) at<h8>(dst + (6 + f) * kFrag, lane * 16) = x.lo;
+      const Frag y = to_b(P[2 * ks], P[2 * ks + 1]);
+      at<h8>(dst + f * kFrag, lane * 16) = y.hi;
+      if (PP == 2) at<h8>(dst + (6 + f) * kFrag, lane * 16) = y.lo;
     }
-  }
-  if (p.w.PT) {   // wave w: tiles (rows i of tile n, columns j of tile w), n >= w
-    const int j = 16 * wv + r;
-    const float rkj = sRk[j];
-    const double Gj = sG[j];
-    f32x4 P[4];
+    if (p.w.PT) {
+      dst = p.w.PT + ci * (2 * 6 * kFrag);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      P[n] = zero;
-      if (n < wv) continue;
-      const f32x4 qk = frag_mm<NP, KS, NF>(QF + n * KS * kFrag, KF + wv * KS * kFrag, lane, zero);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 16 * n + 4 * g + e;
-        P[n][e] = j <= i ? sRq[i] * rkj * exp2_fast(static_cast<float>(sG[i] - Gj)) * qk[e] : 0.0f;
+      for (int ks = 0; ks < 2; ++ks) {
+        if (ks == 0 && wv >= 2) continue;
+        const int f = wv < 2 ? 2 * wv + ks : 2 + wv;
+        const Frag y = to_b(PT[2 * ks], PT[2 * ks + 1]);
+        at<h8>(dst + f * kFrag, lane * 16) = y.hi;
+        at<h8>(dst + (6 + f) * kFrag, lane * 16) = y.lo;
       }
-    }
-    uint16_t* dst = p.w.PT + ci * (2 * 6 * kFrag);
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      if (ks == 0 && wv >= 2) continue;
-      const int f = wv < 2 ? 2 * wv + ks : 2 + wv;
-      const Frag x = to_b(P[2 * ks], P[2 * ks + 1]);
-      at<h8>(dst + f * kFrag, lane * 16) = x.hi;
-      at<h8>(dst + (6 + f) * kFrag, lane * 16) = x.lo;
     }
   }
   __syncthreads();
   if (wv == 0) {   // the four diagonal blocks: a lane solves one column
     float t[16];
-    const float* a = sA + (16 * g) * kAS + 16 * g;
+    float* a = sA + (16 * g) * kAS + 16 * g;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float s = i == r ? 1.0f : 0.0f;
+      float s[2] = {i == r ? 1.0f : 0.0f, 0.0f};   // two chains
 #pragma unroll
-      for (int j = 0; j < i; ++j) s = fmaf(-a[i * kAS + j], t[j], s);
-      t[i] = s;
-      sT[(16 * g + i) * kAS + 16 * g + r] = s;
+      for (int j = 0; j < i; ++j) s[j & 1] = fmaf(-a[i * kAS + j], t[j], s[j & 1]);
+      t[i] = s[0] + s[1];
     }
+    mscan::wave_lds_sync();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a[i * kAS + r] = t[i];
   }
   __syncthreads();
   if (wv < 2) {    // blocks (1, 0) and (3, 2)
     const int o = 32 * wv;
-    const f32x4 x = tile_mm(sA + (o + 16) * kAS + o, sT + o * kAS + o, r, g, zero);
-    const f32x4 y = tile_mm(sT + (o + 16) * kAS + o + 16, x, r, g, zero);
+    const f32x4 y = tile_mm(sA + (o + 16) * kAS + o + 16, tile_mm(sA + (o + 16) * kAS + o, sA + o * kAS + o, r, g, zero), r, g, zero);
+    mscan::wave_lds_sync();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sT[(o + 16 + 4 * g + e) * kAS + o + r] = -y[e];
+    for (int e = 0; e < 4; ++e) sA[(o + 16 + 4 * g + e) * kAS + o + r] = -y[e];
   }
   __syncthreads();
-  if (wv < 2) {    // the lower left 32 x 32 block, one 16-column strip a wave
-    f32x4 x[2];
+  f32x4 z[2];      // the lower left 32 x 32 block, one 16-column strip a wave
+  if (wv < 2) {
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi) {
-      x[mi] = zero;
+      z[mi] = zero;
       for (int kk = wv; kk < 2; ++kk)
-        x[mi] = tile_mm(sA + (32 + 16 * mi) * kAS + 16 * kk, sT + 16 * kk * kAS + 16 * wv, r, g, x[mi]);
+        z[mi] = tile_mm(sA + (32 + 16 * mi) * kAS + 16 * kk, sA + 16 * kk * kAS + 16 * wv, r, g, z[mi]);
     }
+  }
+  __syncthreads();
+  if (wv < 2) {
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi) {
       f32x4 y = zero;
 #pragma unroll
-      for (int kk = 0; kk <= mi; ++kk) y = tile_mm(sT + (32 + 16 * mi) * kAS + 32 + 16 * kk, x[kk], r, g, y);
+      for (int kk = 0; kk <= mi; ++kk) y = tile_mm(sA + (32 + 16 * mi) * kAS + 32 + 16 * kk, z[kk], r, g, y);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sT[(32 + 16 * mi + 4 * g + e) * kAS + 16 * wv + r] = -y[e];
+      for (int e = 0; e < 4; ++e) sA[(32 + 16 * mi + 4 * g + e) * kAS + 16 * wv + r] = -y[e];
     }
   }
   __syncthreads();
   uint16_t* T = p.w.T + ci * (12 * kFrag);
-  uint16_t* TT = p.w.TT ? p.w.TT + ci * (12 * kFrag) : nullptr;
-  for (int it = tid; it < 2 * 6 * 64; it += 256) {
-    const bool tr = it >= 6 * 64;
-    if (tr && !TT) break;
-    const int f = (it >> 6) % 6, i = 16 * (tr ? kUm[f] : kLm[f]) + r, k0 = 32 * (tr ? kUk[f] : kLk[f]);
-    u32x4 hi, lo;
+  for (int f = wv; f < 6; f += 4) {
+    // rows of T: two runs of four columns; the second run of fragments 0 and 3 is above the diagonal
+    const float* a = sA + (16 * kLm[f] + r) * kAS + 32 * kLk[f] + 4 * g;
+    const f32x4 u = *reinterpret_cast<const f32x4*>(a), v = f == 0 || f == 3 ? zero : *reinterpret_cast<const f32x4*>(a + 16);
+    const Frag y = to_b(u, v);
+    at<h8>(T + f * kFrag, lane * 16) = y.hi;
+    at<h8>(T + (6 + f) * kFrag, lane * 16) = y.lo;
+  }
+  if (p.w.TT) {
+    T = p.w.TT + ci * (12 * kFrag);
+    for (int f = wv; f < 6; f += 4) {
+      // columns of T: the first run of fragments 2 (tile 1, step 0) and 5 (tile 3, step 1) is above the diagonal
+      const float* a = sA + (32 * kUk[f] + 4 * g) * kAS + 16 * kUm[f] + r;
+      f32x4 u = zero, v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float v[2];
-#pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const int s = 2 * e + o, x = k0 + (s < 4 ? 4 * g + s : 16 + 4 * g + s - 4);
-        v[o] = tr ? (x >= i ? sT[x * kAS + i] : 0.0f) : (x <= i ? sT[i * kAS + x] : 0.0f);
+      for (int e = 0; e < 4; ++e) {
+        if (f != 2 && f != 5) u[e] = a[e * kAS];
+        v[e] = a[(16 + e) * kAS];
       }
-      uint32_t a, bb;
-      split2(v[0], v[1], a, bb);
-      hi[e] = a;
-      lo[e] = bb;
+      const Frag y = to_b(u, v);
+      at<h8>(T + f * kFrag, lane * 16) = y.hi;
+      at<h8>(T + (6 + f) * kFrag, lane * 16) = y.lo;
     }
-    uint16_t* dst = (tr ? TT : T) + f * kFrag + lane * 8;
-    *reinterpret_cast<u32x4*>(dst) = hi;
-    *reinterpret_cast<u32x4*>(dst + 6 * kFrag) = lo;
   }
 }
 
