@@ -197,7 +197,17 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
     }
     if (c == 0 && p.h0) {
       float m0 = 0.0f;
-      for (int i = tid; i < d.V * d.K; i += 256) m0 = max_finite(m0, p.h0[bh * d.V * d.K + i]);
+      const float* h0 = p.h0 + bh * d.V * d.K;
+      for (int i0 = tid * 4; i0 < d.V * d.K; i0 += 8 * 1024) {   // eight loads in flight: this workgroup would be the last
+        f32x4 y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          y[k] = i0 + k * 1024 < d.V * d.K ? *reinterpret_cast<const f32x4*>(h0 + i0 + k * 1024) : zero;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m0 = max_finite(m0, y[k][e]);
+      }
       m = fmaxf(m, m0 * sqrtf(static_cast<float>(d.K)));
     }
     m = wave_max(m);
