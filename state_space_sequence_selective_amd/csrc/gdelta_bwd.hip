@@ -23,7 +23,8 @@ __global__ void __launch_bounds__(256) gdelta_dymax_kernel(const BwdArgs p) {
   __shared__ float s[4];
   const Dims& d = p.d;
   const int tid = threadIdx.x;
-  const int64_t c = blockIdx.x % d.nc, bh = blockIdx.x / d.nc, h = bh % d.H, b = bh / d.H;
+  const ChunkPlace at_ = chunk_place(blockIdx.x, static_cast<uint32_t>(d.H), static_cast<uint32_t>(d.nc));
+  const int64_t c = at_.c, h = at_.h, b = at_.b, bh = b * d.H + h;
   const int64_t t0 = c * kC, left = d.T - t0;
   float m = 0.0f;
   const int row = tid >> 2;   // four threads a row, four loads in flight
@@ -329,8 +330,8 @@ __global__ void __launch_bounds__(256, SHARED && KP == 128 ? 1 : 2) gdelta_bwd_c
   const Dims& d = p.d;
   int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wv = wave_id();
-  const uint32_t nc32 = static_cast<uint32_t>(d.nc), G32 = static_cast<uint32_t>(d.G);
-  const int64_t c = blockIdx.x % nc32, bg = blockIdx.x / nc32, hk = bg % G32, b = static_cast<uint32_t>(bg) / G32;
+  const ChunkPlace at_ = chunk_place(blockIdx.x, static_cast<uint32_t>(d.G), static_cast<uint32_t>(d.nc));
+  const int64_t c = at_.c, hk = at_.h, b = at_.b, bg = b * d.G + hk;
   const int64_t t0 = c * kC, left = d.T - t0, gi = bg * d.nc + c;
   const int share = SHARED ? static_cast<int>(d.H / d.G) : 1;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};

@@ -14,8 +14,9 @@ __global__ void __launch_bounds__(256) gdelta_rows_kernel(const FwdArgs p) {
   __shared__ __attribute__((aligned(16))) uint16_t s[2][NP][kC * ROW];
   const Dims& d = p.d;
   const int tid = threadIdx.x, lane = tid & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
-  const int64_t c = blockIdx.x % d.nc, bg = blockIdx.x / d.nc, hk = bg % d.G, b = bg / d.G;
-  const int64_t t0 = c * kC, left = d.T - t0, ci = bg * d.nc + c;
+  const ChunkPlace at_ = chunk_place(blockIdx.x, static_cast<uint32_t>(d.G), static_cast<uint32_t>(d.nc));
+  const int64_t c = at_.c, hk = at_.h, b = at_.b;
+  const int64_t t0 = c * kC, left = d.T - t0, ci = (b * d.G + hk) * d.nc + c;
   float* sc = p.w.gsc + ci * (kGroupSc * kC);
   const int row = tid >> 2, part = tid & 3;   // four threads a row
   const int64_t base = ((b * d.T + t0 + row) * d.G + hk) * d.K;
@@ -126,7 +127,7 @@ __device__ __forceinline__ f32x4 tile_mm(const float* a, f32x4 b, int r, int g, 
 }
 
 template <Act A, int KP>
-__global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
+__global__ void __launch_bounds__(256, 5) gdelta_prep_kernel(const FwdArgs p) {
   constexpr int NP = A == Act::F32 ? 2 : 1, KS = KP / 32, NF = KP / 8;
   __shared__ __attribute__((aligned(16))) float sA[kC * kAS];   // A, and block by block its place taken by T
   __shared__ double sG[kC];
@@ -134,23 +135,17 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
   __shared__ float sMax[4];
   const Dims& d = p.d;
   const int tid = threadIdx.x, lane = tid & 63, wv = wave_id(), r = lane & 15, g = lane >> 4;
-  const uint32_t nc32 = static_cast<uint32_t>(d.nc), H32 = static_cast<uint32_t>(d.H);
-  const uint32_t head = blockIdx.x / nc32;
-  const int64_t c = blockIdx.x % nc32, bh = head, h = head % H32, b = head / H32, hk = (head % H32) / (H32 / static_cast<uint32_t>(d.G));
+  const ChunkPlace at_ = chunk_place(blockIdx.x, static_cast<uint32_t>(d.H), static_cast<uint32_t>(d.nc));
+  const int64_t c = at_.c, h = at_.h, b = at_.b, bh = b * d.H + h, hk = at_.h / (static_cast<uint32_t>(d.H) / static_cast<uint32_t>(d.G));
   const int64_t t0 = c * kC, left = d.T - t0, ci = bh * d.nc + c, gi = (b * d.G + hk) * d.nc + c;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   const uint16_t* KF = p.w.KF + gi * (NP * NF * kFrag);
   const uint16_t* QF = p.w.QF + gi * (NP * NF * kFrag);
-  // Wave w's operands: k of tiles 0 .. w, q of tiles w .. 3 (five tiles), and k and q of tile w; all in flight while the
-  // gates are made.  A slot s <= w gives the tile (rows j of s, columns i of w) of k.k^T and k.q^T, a later one (rows i
-  // of s - 1, columns j of w) of q.k^T.
-  h8 x[5][KS], bk[KS], bq[KS];
-#pragma unroll
-  for (int s = 0; s < 5; ++s) {
-    const uint16_t* src = s <= wv ? KF + s * KS * kFrag : QF + (s - 1) * KS * kFrag;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) x[s][ks] = at<h8>(src + ks * kFrag, lane * 16);
-  }
+  // Wave w's operands: k of tiles 0 .. w, q of tiles w .. 3 (five tiles), and k and q of tile w, in flight while the gates
+  // are made.  A slot s <= w gives the tile (rows j of s, columns i of w) of k.k^T and k.q^T, a later one (rows i of
+  // s - 1, columns j of w) of q.k^T.  (All five tiles in flight would take 80 more registers, and two of five workgroups a
+  // CU.)
+  h8 bk[KS], bq[KS];
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
     bk[ks] = at<h8>(KF + (wv * KS + ks) * kFrag, lane * 16);
@@ -225,20 +220,23 @@ __global__ void __launch_bounds__(256) gdelta_prep_kernel(const FwdArgs p) {
 #pragma unroll
     for (int s = 0; s < 5; ++s) {
       f32x4 xk = zero, xq = zero;
+      const uint16_t* src = s <= wv ? KF + s * KS * kFrag : QF + (s - 1) * KS * kFrag;
+      h8 x[KS];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) x[ks] = at<h8>(src + ks * kFrag, lane * 16);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        xk = mma(x[s][ks], bk[ks], xk);
-        xq = mma(x[s][ks], bq[ks], xq);
+        xk = mma(x[ks], bk[ks], xk);
+        xq = mma(x[ks], bq[ks], xq);
       }
       if (NP == 2) {   // the planes of low parts
-        const uint16_t* src = s <= wv ? KF + s * KS * kFrag : QF + (s - 1) * KS * kFrag;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           const h8 xl = at<h8>(src + (NF + ks) * kFrag, lane * 16);
           xk = mma(xl, bk[ks], xk);
           xq = mma(xl, bq[ks], xq);
-          xk = mma(x[s][ks], at<h8>(KF + (NF + wv * KS + ks) * kFrag, lane * 16), xk);
-          xq = mma(x[s][ks], at<h8>(QF + (NF + wv * KS + ks) * kFrag, lane * 16), xq);
+          xk = mma(x[ks], at<h8>(KF + (NF + wv * KS + ks) * kFrag, lane * 16), xk);
+          xq = mma(x[ks], at<h8>(QF + (NF + wv * KS + ks) * kFrag, lane * 16), xq);
         }
       }
       if (s <= wv) {   // rows j, column i
