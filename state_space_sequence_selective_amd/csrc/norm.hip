@@ -1,17 +1,19 @@
 // Layer norm, forward and backward (gfx950), and the entry points of
 // include/mamba_norm.h.
 //
-// A team of 16, 64, 256 or 1024 lanes holds one row in registers, eight
-// elements a lane and step, so a row is read once: the mean, the centred sum
-// of squares and the output all come from registers.  The backward keeps the
-// columns' sums for d_w and d_b in registers over the rows its workgroup
-// walks, writes one partial row per workgroup, and a second launch adds the
-// partials in a fixed order (no atomics).  Both are bound by HBM.
+// A team of 8 to 1024 lanes holds one row in registers, a 16-byte piece a lane
+// and step, so a row is read once: the mean, the centred sum of squares and
+// the output all come from registers.  The backward keeps the columns' sums
+// for d_w and d_b in registers over the rows its workgroup walks (the next
+// row's loads in flight), writes one partial row per workgroup, and a second
+// launch adds the partials in a fixed order (no atomics).  Both are bound by
+// HBM.
 #include <cmath>
 #include <string>
 
 #include "mamba_norm.h"
 #include "scan_common.h"
+#include "wave_ops.h"
 
 namespace mscan {
 void set_last_error(const std::string& msg);   // abi.hip
@@ -21,9 +23,6 @@ namespace lnorm {
 
 using mscan::Act;
 using mscan::IO;
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 struct Args {
   int64_t rows;
@@ -38,42 +37,39 @@ struct Args {
   int blocks;
 };
 
-// Eight elements from index i, the first n of them inside the row.  Rows of an odd length start at any element, so
-// the vector accesses claim no more than the element's own alignment.
-template <Act A>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int n, float* out) {
-  constexpr int S = A == Act::F32 ? 4 : 2;
-  const char* src = static_cast<const char*>(p) + i * S;
-  if (n >= 8) {
-    uint32_t w[2 * S];
-    __builtin_memcpy(w, __builtin_assume_aligned(src, S), 8 * S);
+// E elements of type A as they lie in memory
+template <Act A, int E>
+struct Piece {
+  static constexpr int S = A == Act::F32 ? 4 : 2, W = E * S / 4;
+  uint32_t w[W];
+
+  // from element i on, the first n of them inside the row.  Rows of an odd length start at any element, so the vector
+  // accesses claim no more than the element's own alignment.
+  __device__ __forceinline__ void load(const void* p, int64_t i, int n) {
+    const char* src = static_cast<const char*>(p) + i * S;
+    if (n >= E) {
+      __builtin_memcpy(w, __builtin_assume_aligned(src, S), E * S);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (A == Act::F32) out[e] = __builtin_bit_cast(float, w[e]);
-      else out[e] = IO<A>::cvt((e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu);
+      for (int k = 0; k < W; ++k) w[k] = 0u;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e < n) w[e * S / 4] |= IO<A>::ldraw(p, i + e) << (S == 2 && (e & 1) ? 16 : 0);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = e < n ? IO<A>::ld(p, i + e) : 0.0f;
   }
-}
-
-__device__ __forceinline__ void load8w(const float* p, int i, int n, float fill, float* out) {
-  if (!p) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = fill;
-  } else {
-    load8<Act::F32>(p, i, n, out);
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (S == 4) return __builtin_bit_cast(float, w[e]);
+    else return IO<A>::cvt((e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu);
   }
-}
+};
 
-template <Act A>
-__device__ __forceinline__ void store8(void* p, int64_t i, int n, const float* v) {
+template <Act A, int E>
+__device__ __forceinline__ void store_piece(void* p, int64_t i, int n, const float* v) {
   constexpr int S = A == Act::F32 ? 4 : 2;
-  if (n >= 8) {
-    uint32_t w[2 * S];
+  if (n >= E) {
+    uint32_t w[E * S / 4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < E; ++e) {
       if constexpr (A == Act::F32) {
         w[e] = __builtin_bit_cast(uint32_t, v[e]);
       } else {
@@ -83,23 +79,35 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int n, const float* v
         w[e / 2] = (e & 1) ? w[e / 2] | (static_cast<uint32_t>(h) << 16) : h;
       }
     }
-    __builtin_memcpy(__builtin_assume_aligned(static_cast<char*>(p) + i * S, S), w, 8 * S);
+    __builtin_memcpy(__builtin_assume_aligned(static_cast<char*>(p) + i * S, S), w, E * S);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < E; ++e)
       if (e < n) IO<A>::st(p, i + e, v[e]);
+  }
+}
+
+template <int E>
+__device__ __forceinline__ void load_weight(const float* p, int i, int n, float fill, float* out) {
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = fill;
+  } else {
+    Piece<Act::F32, E> x;
+    x.load(p, i, n);
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = x.get(e);
   }
 }
 
 // Sum over a team; every lane gets it.  `s`: one float per wave and slot.
 template <int TEAM>
 __device__ __forceinline__ float team_sum(float v, float* s) {
-  constexpr int W = TEAM < 64 ? TEAM : 64;
-#pragma unroll
-  for (int o = 1; o < W; o <<= 1) v += __shfl_xor(v, o, 64);
+  if constexpr (TEAM == 8) return waveops::sum8(v);
+  if constexpr (TEAM == 16) return waveops::sum16(v);
+  v = waveops::wave_sum(v);
   if constexpr (TEAM > 64) {
-    const int wv = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) s[wv] = v;
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0.0f;
 #pragma unroll
@@ -108,82 +116,126 @@ __device__ __forceinline__ float team_sum(float v, float* s) {
   return v;
 }
 
+// elements of a lane's piece: 16 bytes of the wider type
+template <Act X, Act Y>
+constexpr int kPiece = X == Act::F32 || Y == Act::F32 ? 4 : 8;
+
+// A workgroup walks rows too: w and b stay in its registers (read again for every row they would be more than the row:
+// 40 KB of 5120 columns against 20), and the next row's loads are in flight.
 template <Act X, Act Y, int TEAM, int NV>
 __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) norm_fwd_kernel(const Args p) {
-  constexpr int BLOCK = TEAM < 256 ? 256 : TEAM, TEAMS = BLOCK / TEAM;
-  __shared__ float s[2][BLOCK / 64];
+  constexpr int BLOCK = TEAM < 256 ? 256 : TEAM, TEAMS = BLOCK / TEAM, E = kPiece<X, Y>;
+  __shared__ float s[2][2][BLOCK / 64];
   const int lane = threadIdx.x % TEAM;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TEAM;
-  if (TEAM < 64 || TEAM == 64) {
-    if (row >= p.rows) return;   // whole teams; no barrier below for them
-  }
-  float x[NV][8];
-  float sum = 0.0f;
+  const float inv = 1.0f / static_cast<float>(p.dim);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / TEAM;
+  Piece<X, E> raw[NV];
+  auto load = [&](int64_t r) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = 8 * (lane + i * TEAM);
-    load8<X>(p.x, row * p.dim + col, p.dim - col, x[i]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum += x[i][e];
-  }
-  const float inv = 1.0f / static_cast<float>(p.dim), mean = team_sum<TEAM>(sum, s[0]) * inv;
-  float sq = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int n = p.dim - 8 * (lane + i * TEAM);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[i][e] = e < n ? x[i][e] - mean : 0.0f;
-      sq = fmaf(x[i][e], x[i][e], sq);
+    for (int i = 0; i < NV; ++i) {
+      const int col = E * (lane + i * TEAM);
+      raw[i].load(p.x, r * p.dim + col, r < p.rows ? p.dim - col : 0);
     }
-  }
-  const float rstd = 1.0f / sqrtf(team_sum<TEAM>(sq, s[1]) * inv + p.eps);
+  };
+  load(row);
+  float w[NV][E], b[NV][E];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = 8 * (lane + i * TEAM), n = p.dim - col;
-    if (n <= 0) continue;
-    float w[8], b[8];
-    load8w(p.w, col, n, 1.0f, w);
-    load8w(p.b, col, n, 0.0f, b);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[i][e] = fmaf(x[i][e] * rstd, w[e], b[e]);
-    store8<Y>(p.y, row * p.dim + col, n, x[i]);
+    const int col = E * (lane + i * TEAM);
+    load_weight<E>(p.w, col, p.dim - col, 1.0f, w[i]);
+    load_weight<E>(p.b, col, p.dim - col, 0.0f, b[i]);
   }
-  if (lane == 0 && p.mean) {
-    p.mean[row] = mean;
-    p.rstd[row] = rstd;
+  int turn = 0;
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * TEAMS; row0 < p.rows; row0 += stride, row += stride) {
+    const bool ok = row < p.rows;
+    float x[NV][E];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        x[i][e] = raw[i].get(e);
+        sum += x[i][e];
+      }
+    load(row + stride);
+    const float mean = team_sum<TEAM>(sum, s[turn][0]) * inv;
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int n = p.dim - E * (lane + i * TEAM);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        x[i][e] = e < n ? x[i][e] - mean : 0.0f;
+        sq = fmaf(x[i][e], x[i][e], sq);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(team_sum<TEAM>(sq, s[turn][1]) * inv + p.eps);
+    turn ^= 1;   // the next row's sums go to the other slots: a barrier lies between this row's reads and those
+    if (!ok) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = E * (lane + i * TEAM), n = p.dim - col;
+      if (n <= 0) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[i][e] = fmaf(x[i][e] * rstd, w[i][e], b[i][e]);
+      store_piece<Y, E>(p.y, row * p.dim + col, n, x[i]);
+    }
+    if (lane == 0 && p.mean) {
+      p.mean[row] = mean;
+      p.rstd[row] = rstd;
+    }
   }
 }
 
 template <Act X, Act Y, int TEAM, int NV>
 __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) norm_bwd_kernel(const Args p) {
-  constexpr int BLOCK = TEAM < 256 ? 256 : TEAM, TEAMS = BLOCK / TEAM;
+  constexpr int BLOCK = TEAM < 256 ? 256 : TEAM, TEAMS = BLOCK / TEAM, E = kPiece<X, Y>;
   __shared__ float s[2][2][BLOCK / 64];
-  __shared__ float cols[TEAMS > 1 ? 2 * TEAM * NV * 8 : 1];
+  __shared__ float cols[TEAMS > 1 ? 2 * TEAM * NV * E : 1];
   const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
-  float dw[NV][8], db[NV][8];
+  float dw[NV][E], db[NV][E];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.0f;
+    for (int e = 0; e < E; ++e) dw[i][e] = db[i][e] = 0.0f;
   const float inv = 1.0f / static_cast<float>(p.dim);
+  // the row at work and the next one, as they lie in memory
+  Piece<X, E> rx[NV], ra[NV];
+  Piece<Y, E> ry[NV];
+  float rmean, rrstd;
+  auto load = [&](int64_t row) {
+    const bool ok = row < p.rows;
+    rmean = ok ? p.mean[row] : 0.0f;
+    rrstd = ok ? p.rstd[row] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = E * (lane + i * TEAM), left = ok ? p.dim - col : 0;
+      rx[i].load(p.x, row * p.dim + col, left);
+      ry[i].load(p.dy, row * p.dim + col, left);
+      if (p.d_add) ra[i].load(p.d_add, row * p.dim + col, left);
+    }
+  };
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * TEAMS;
+  int64_t row0 = static_cast<int64_t>(blockIdx.x) * TEAMS;
+  load(row0 + team);
   int turn = 0;
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * TEAMS; row0 < p.rows; row0 += static_cast<int64_t>(gridDim.x) * TEAMS) {
+  for (; row0 < p.rows; row0 += stride) {
     const int64_t row = row0 + team;
     const bool ok = row < p.rows;
-    const float mean = ok ? p.mean[row] : 0.0f, rstd = ok ? p.rstd[row] : 0.0f;
-    float n[NV][8], dn[NV][8];
+    const float mean = rmean, rstd = rrstd;
+    float n[NV][E], dn[NV][E], add[NV][E];
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = 8 * (lane + i * TEAM), left = ok ? p.dim - col : 0;
-      load8<X>(p.x, row * p.dim + col, left, n[i]);
-      load8<Y>(p.dy, row * p.dim + col, left, dn[i]);
-      float w[8];
-      load8w(p.w, col, p.dim - col, 1.0f, w);
+      const int col = E * (lane + i * TEAM), left = ok ? p.dim - col : 0;
+      float w[E];
+      load_weight<E>(p.w, col, p.dim - col, 1.0f, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        n[i][e] = e < left ? (n[i][e] - mean) * rstd : 0.0f;
+      for (int e = 0; e < E; ++e) {
+        n[i][e] = e < left ? (rx[i].get(e) - mean) * rstd : 0.0f;
+        dn[i][e] = ry[i].get(e);
+        add[i][e] = p.d_add ? ra[i].get(e) : 0.0f;
         db[i][e] += dn[i][e];
         dw[i][e] = fmaf(dn[i][e], n[i][e], dw[i][e]);
         dn[i][e] *= w[e];
@@ -191,21 +243,17 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) norm_bwd_kernel(const
         s2 = fmaf(dn[i][e], n[i][e], s2);
       }
     }
+    load(row + stride);
     s1 = team_sum<TEAM>(s1, s[turn][0]) * inv;
     s2 = team_sum<TEAM>(s2, s[turn][1]) * inv;
     turn ^= 1;   // the next row's sums go to the other slots: a barrier lies between this row's reads and those
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = 8 * (lane + i * TEAM), left = ok ? p.dim - col : 0;
+      const int col = E * (lane + i * TEAM), left = ok ? p.dim - col : 0;
       if (left <= 0) continue;
-      float add[8];
-      if (p.d_add) load8<X>(p.d_add, row * p.dim + col, left, add);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = rstd * (dn[i][e] - s1 - n[i][e] * s2);
-        n[i][e] = p.d_add ? v + add[e] : v;
-      }
-      store8<X>(p.dx, row * p.dim + col, left, n[i]);
+      for (int e = 0; e < E; ++e) n[i][e] = fmaf(rstd, dn[i][e] - s1 - n[i][e] * s2, add[i][e]);
+      store_piece<X, E>(p.dx, row * p.dim + col, left, n[i]);
     }
   }
   if (!p.part) return;
@@ -216,27 +264,27 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) norm_bwd_kernel(const
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float* a = cols + (i * 8 + e) * TEAM + lane;
+          for (int e = 0; e < E; ++e) {
+            float* a = cols + (i * E + e) * TEAM + lane;
             a[0] = (k ? a[0] : 0.0f) + dw[i][e];
-            a[NV * 8 * TEAM] = (k ? a[NV * 8 * TEAM] : 0.0f) + db[i][e];
+            a[NV * E * TEAM] = (k ? a[NV * E * TEAM] : 0.0f) + db[i][e];
           }
       }
       __syncthreads();
     }
     for (int c = threadIdx.x; c < p.dim; c += BLOCK) {
-      const int l = (c / 8) % TEAM, i = (c / 8) / TEAM, e = c % 8;
-      const float* a = cols + (i * 8 + e) * TEAM + l;
+      const int l = (c / E) % TEAM, i = (c / E) / TEAM, e = c % E;
+      const float* a = cols + (i * E + e) * TEAM + l;
       part[c] = a[0];
-      part[p.dim + c] = a[NV * 8 * TEAM];
+      part[p.dim + c] = a[NV * E * TEAM];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = 8 * (lane + i * TEAM), n = p.dim - col;
+      const int col = E * (lane + i * TEAM), n = p.dim - col;
       if (n <= 0) continue;
-      store8<Act::F32>(part, col, n, dw[i]);
-      store8<Act::F32>(part, p.dim + col, n, db[i]);
+      store_piece<Act::F32, E>(part, col, n, dw[i]);
+      store_piece<Act::F32, E>(part, p.dim + col, n, db[i]);
     }
   }
 }
@@ -248,8 +296,13 @@ __global__ void __launch_bounds__(1024) norm_colsum_kernel(const Args p) {
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 16 + c;
   const int64_t n = 2 * static_cast<int64_t>(p.dim);
   float acc = 0.0f;
-  if (col < n)
-    for (int r = strip; r < p.blocks; r += 64) acc += p.part[r * n + col];
+  for (int r0 = strip; r0 < p.blocks; r0 += 64 * 8) {   // eight loads in flight
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = col < n && r0 + 64 * k < p.blocks ? p.part[(r0 + 64 * k) * n + col] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc += v[k];
+  }
   s[strip][c] = acc;
   __syncthreads();
 #pragma unroll
@@ -302,51 +355,81 @@ int check_ptr(const char* name, const void* p, bool need, int align) {
     if (e_ != hipSuccess) return fail(MAMBA_ERR_HIP, std::string(#expr) + ": " + hipGetErrorString(e_)); \
   } while (0)
 
-// rows a workgroup works on at once
-int teams_of(int dim) { return dim <= 256 ? 16 : dim <= 2048 ? 4 : 1; }
+// How a row is laid over lanes: the smallest team that holds it in at most 32 (few rows: 8) elements a lane.
+struct Shape {
+  int team, nv;
+};
 
-// Workgroups of the backward: at most 1024 (four for each CU), each with a partial row of d_w and d_b.
-int bwd_blocks(const mamba_norm_dims_t& d) {
-  const int64_t n = (d.rows + teams_of(static_cast<int>(d.dim)) - 1) / teams_of(static_cast<int>(d.dim));
-  return static_cast<int>(n < 1024 ? n : 1024);
+Shape shape_of(const mamba_norm_dims_t& d) {
+  const int e = d.x == MAMBA_F32 || d.y == MAMBA_F32 ? 4 : 8;
+  const int pieces = static_cast<int>((d.dim + e - 1) / e);
+  if (pieces <= 8) return {8, 1};
+  if (pieces <= 16) return {16, 1};
+  if (pieces <= 32) return {16, 2};
+  if (pieces <= 64 * 2) return {64, (pieces + 63) / 64};
+  if (pieces <= 64 * 4 && d.rows > 1024) return {64, 4};
+  const int per = (pieces + 255) / 256;
+  if (per * e <= 32) return {256, per == 7 ? 8 : per};
+  return {1024, 16 / e};
 }
 
-size_t part_bytes(const mamba_norm_dims_t& d) { return static_cast<size_t>(bwd_blocks(d)) * 2 * d.dim * 4; }
+// Workgroups that walk the rows: four rows each at least, if that leaves 256 of them, and at most 1024 (four for each CU).
+// In the backward each has a partial row of d_w and d_b.
+int walkers(const mamba_norm_dims_t& d) {
+  const int team = shape_of(d).team, teams = team < 256 ? 256 / team : 1;
+  const int64_t steps = (d.rows + teams - 1) / teams, quarter = (steps + 3) / 4;
+  if (steps <= 256) return static_cast<int>(steps);
+  return static_cast<int>(quarter < 256 ? 256 : quarter < 1024 ? quarter : 1024);
+}
+
+size_t part_bytes(const mamba_norm_dims_t& d) { return static_cast<size_t>(walkers(d)) * 2 * d.dim * 4; }
 
 template <Act X, Act Y, int TEAM, int NV, bool BWD>
 hipError_t launch_team(const Args& a, hipStream_t st) {
-  constexpr int BLOCK = TEAM < 256 ? 256 : TEAM, TEAMS = BLOCK / TEAM;
+  constexpr int BLOCK = TEAM < 256 ? 256 : TEAM;
   if (BWD) hipLaunchKernelGGL((norm_bwd_kernel<X, Y, TEAM, NV>), dim3(a.blocks), dim3(BLOCK), 0, st, a);
-  else
-    hipLaunchKernelGGL((norm_fwd_kernel<X, Y, TEAM, NV>), dim3(static_cast<unsigned>((a.rows + TEAMS - 1) / TEAMS)),
-                       dim3(BLOCK), 0, st, a);
+  else hipLaunchKernelGGL((norm_fwd_kernel<X, Y, TEAM, NV>), dim3(a.blocks), dim3(BLOCK), 0, st, a);
   return hipGetLastError();
 }
 
 template <Act X, Act Y, bool BWD>
-hipError_t launch_xy(const Args& a, hipStream_t st) {
-  if (a.dim <= 128) return launch_team<X, Y, 16, 1, BWD>(a, st);
-  if (a.dim <= 256) return launch_team<X, Y, 16, 2, BWD>(a, st);
-  if (a.dim <= 512) return launch_team<X, Y, 64, 1, BWD>(a, st);
-  if (a.dim <= 1024) return launch_team<X, Y, 64, 2, BWD>(a, st);
-  if (a.dim <= 2048) return launch_team<X, Y, 64, 4, BWD>(a, st);
-  if (a.dim <= 4096) return launch_team<X, Y, 256, 2, BWD>(a, st);
-  if (a.dim <= 8192) return launch_team<X, Y, 256, 4, BWD>(a, st);
-  return launch_team<X, Y, 1024, 2, BWD>(a, st);
+hipError_t launch_xy(const Shape& s, const Args& a, hipStream_t st) {
+  constexpr int E = kPiece<X, Y>;
+  if (s.team == 8) return launch_team<X, Y, 8, 1, BWD>(a, st);
+  if (s.team == 16) return s.nv == 1 ? launch_team<X, Y, 16, 1, BWD>(a, st) : launch_team<X, Y, 16, 2, BWD>(a, st);
+  if (s.team == 64) {
+    if (s.nv == 1) return launch_team<X, Y, 64, 1, BWD>(a, st);
+    return s.nv == 2 ? launch_team<X, Y, 64, 2, BWD>(a, st) : launch_team<X, Y, 64, 4, BWD>(a, st);
+  }
+  if (s.team == 1024) return launch_team<X, Y, 1024, 16 / E, BWD>(a, st);
+  switch (s.nv) {
+    case 1: return launch_team<X, Y, 256, 1, BWD>(a, st);
+    case 2: return launch_team<X, Y, 256, 2, BWD>(a, st);
+    case 3: return launch_team<X, Y, 256, 3, BWD>(a, st);
+    case 4: return launch_team<X, Y, 256, 4, BWD>(a, st);
+    default: break;
+  }
+  if constexpr (E == 4) {
+    if (s.nv == 5) return launch_team<X, Y, 256, 5, BWD>(a, st);
+    if (s.nv == 6) return launch_team<X, Y, 256, 6, BWD>(a, st);
+    return launch_team<X, Y, 256, 8, BWD>(a, st);
+  }
+  return hipErrorInvalidValue;
 }
 
 template <bool BWD>
-hipError_t launch(int x, int y, const Args& a, hipStream_t st) {
-  switch (x * 3 + y) {
-    case 0: return launch_xy<Act::F32, Act::F32, BWD>(a, st);
-    case 1: return launch_xy<Act::F32, Act::BF16, BWD>(a, st);
-    case 2: return launch_xy<Act::F32, Act::F16, BWD>(a, st);
-    case 3: return launch_xy<Act::BF16, Act::F32, BWD>(a, st);
-    case 4: return launch_xy<Act::BF16, Act::BF16, BWD>(a, st);
-    case 5: return launch_xy<Act::BF16, Act::F16, BWD>(a, st);
-    case 6: return launch_xy<Act::F16, Act::F32, BWD>(a, st);
-    case 7: return launch_xy<Act::F16, Act::BF16, BWD>(a, st);
-    default: return launch_xy<Act::F16, Act::F16, BWD>(a, st);
+hipError_t launch(const mamba_norm_dims_t& d, const Args& a, hipStream_t st) {
+  const Shape s = shape_of(d);
+  switch (d.x * 3 + d.y) {
+    case 0: return launch_xy<Act::F32, Act::F32, BWD>(s, a, st);
+    case 1: return launch_xy<Act::F32, Act::BF16, BWD>(s, a, st);
+    case 2: return launch_xy<Act::F32, Act::F16, BWD>(s, a, st);
+    case 3: return launch_xy<Act::BF16, Act::F32, BWD>(s, a, st);
+    case 4: return launch_xy<Act::BF16, Act::BF16, BWD>(s, a, st);
+    case 5: return launch_xy<Act::BF16, Act::F16, BWD>(s, a, st);
+    case 6: return launch_xy<Act::F16, Act::F32, BWD>(s, a, st);
+    case 7: return launch_xy<Act::F16, Act::BF16, BWD>(s, a, st);
+    default: return launch_xy<Act::F16, Act::F16, BWD>(s, a, st);
   }
 }
 
@@ -376,9 +459,6 @@ int mamba_layernorm_fwd(const mamba_norm_dims_t* dims, const void* x, const floa
   LN_TRY(check_ptr("y", y, true, 16));
   LN_TRY(check_ptr("mean", mean, rstd != nullptr, 4));
   LN_TRY(check_ptr("rstd", rstd, mean != nullptr, 4));
-  const int teams = teams_of(static_cast<int>(dims->dim));
-  if ((dims->rows + teams - 1) / teams >= (int64_t(1) << (dims->dim > 8192 ? 22 : 24)))   // fewer than 2^32 threads
-    return fail(MAMBA_ERR_CAPACITY, "too many rows for one launch");
   Args a{};
   a.rows = dims->rows;
   a.dim = static_cast<int>(dims->dim);
@@ -389,7 +469,8 @@ int mamba_layernorm_fwd(const mamba_norm_dims_t* dims, const void* x, const floa
   a.y = y;
   a.mean = mean;
   a.rstd = rstd;
-  LN_HIP(launch<false>(dims->x, dims->y, a, static_cast<hipStream_t>(stream)));
+  a.blocks = walkers(*dims);
+  LN_HIP(launch<false>(*dims, a, static_cast<hipStream_t>(stream)));
   mscan::set_last_error("");
   return MAMBA_OK;
 }
@@ -427,9 +508,9 @@ int mamba_layernorm_bwd(const mamba_norm_dims_t* dims, const void* x, const floa
   a.d_w = d_w;
   a.d_b = d_b;
   a.part = sums ? static_cast<float*>(workspace) : nullptr;
-  a.blocks = bwd_blocks(*dims);
+  a.blocks = walkers(*dims);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  LN_HIP(launch<true>(dims->x, dims->y, a, st));
+  LN_HIP(launch<true>(*dims, a, st));
   if (sums) {
     hipLaunchKernelGGL(norm_colsum_kernel, dim3(static_cast<unsigned>((2 * dims->dim + 15) / 16)), dim3(1024), 0, st, a);
     LN_HIP(hipGetLastError());
