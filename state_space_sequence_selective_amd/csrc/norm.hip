@@ -373,13 +373,15 @@ Shape shape_of(const mamba_norm_dims_t& d) {
   return {1024, 16 / e};
 }
 
-// Workgroups that walk the rows: four rows each at least, if that leaves 256 of them, and at most 1024 (four for each CU).
-// In the backward each has a partial row of d_w and d_b.
+// Workgroups that walk the rows: four steps each at least, if that leaves 256 of them.  At most two for each CU where a
+// workgroup has one row (their registers fill a CU: 217 us the backward of 16384 x 5120, against 223 with 1024 and half
+// the partial sums), four where it has several (26 us of 196608 x 64 against 30).  In the backward each has a partial row
+// of d_w and d_b.
 int walkers(const mamba_norm_dims_t& d) {
   const int team = shape_of(d).team, teams = team < 256 ? 256 / team : 1;
-  const int64_t steps = (d.rows + teams - 1) / teams, quarter = (steps + 3) / 4;
+  const int64_t steps = (d.rows + teams - 1) / teams, quarter = (steps + 3) / 4, most = teams > 1 ? 1024 : 512;
   if (steps <= 256) return static_cast<int>(steps);
-  return static_cast<int>(quarter < 256 ? 256 : quarter < 1024 ? quarter : 1024);
+  return static_cast<int>(quarter < 256 ? 256 : quarter < most ? quarter : most);
 }
 
 size_t part_bytes(const mamba_norm_dims_t& d) { return static_cast<size_t>(walkers(d)) * 2 * d.dim * 4; }

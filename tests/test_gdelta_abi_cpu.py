@@ -131,7 +131,9 @@ def test_layout(pkg):
         bwd = al(heads * 4) + al(8 * 4) + al(heads * 8) + 2 * al(heads * 64 * 32 * 4)
         assert pkg.gdelta_saved_bytes(gd(pkg, act=act)) == saved
         assert pkg.gdelta_workspace_bytes(gd(pkg, act=act)) == max(fwd, bwd)
-    assert pkg.layernorm_workspace_bytes(ln(pkg, rows=5000, dim=5120)) == 1024 * 2 * 5120 * 4
+    assert pkg.layernorm_workspace_bytes(ln(pkg, rows=5000, dim=5120)) == 512 * 2 * 5120 * 4
+    assert pkg.layernorm_workspace_bytes(ln(pkg, rows=100000, dim=64)) == 1024 * 2 * 64 * 4
+    assert pkg.layernorm_workspace_bytes(ln(pkg, rows=100, dim=5120)) == 100 * 2 * 5120 * 4
 
 
 def test_binding_checks(pkg):
