@@ -67,6 +67,10 @@ int mamba_gdelta_saved_bytes(const mamba_gdelta_dims_t* dims, size_t* bytes);
  * without `saved` and the backward's; one buffer of this size serves both). */
 int mamba_gdelta_workspace_bytes(const mamba_gdelta_dims_t* dims, size_t* bytes);
 
+/* A forward without `saved` takes up to this many tokens one by one, as
+ * mamba_gdelta_step does, and needs no `workspace` for them. */
+#define MAMBA_GDELTA_STEP_TOKENS 8
+
 /* Forward.  h0: f32 or NULL (= zeros); h_last: f32 or NULL.  `saved` is what
  * the backward needs, NULL when none follows; without it `workspace` is used
  * (else it may be NULL). */

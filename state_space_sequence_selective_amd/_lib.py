@@ -470,6 +470,9 @@ def m3_bwd(d: M3Dims, x, b_in, c_in, dd_dt_raw, dd_a_raw, trap_raw, angles_raw, 
 # ----------------------------------------------------- gated delta rule core
 
 
+GDELTA_STEP_TOKENS = 8   # MAMBA_GDELTA_STEP_TOKENS
+
+
 class GDeltaDims(ctypes.Structure):
     """mamba_gdelta_dims_t."""
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("heads", ctypes.c_int64),

@@ -12,8 +12,11 @@ void set_last_error(const std::string& msg);   // abi.hip
 namespace gdelta {
 namespace {
 
-// Sequences up to this long take the token-by-token kernel when nothing is kept for a backward pass.
-constexpr int64_t kStepMaxT = 16;
+// Sequences up to this long take the token-by-token kernel when nothing is kept for a backward pass: 8 tokens of 16 heads
+// of 128 x 128 take 18 us in it against 21 in chunks, 34 against 39 with 16 sequences, 398 against 511 with 256 (15
+// against 17, 23 against 28 and 246 against 305 with 24 heads of 64 x 64); 12 tokens 26 against 21, 49 against 39, 560
+// against 512.
+constexpr int64_t kStepMaxT = MAMBA_GDELTA_STEP_TOKENS;
 
 thread_local const char* g_fn = "";
 

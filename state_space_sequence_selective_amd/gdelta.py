@@ -23,7 +23,7 @@ class GatedDeltaCore:
         kw = dict(device=device)
         self.y = torch.empty(s["v"], dtype=at, **kw)
         self.h_last = torch.empty(s["state"], dtype=f, **kw)
-        self.workspace = torch.empty(_lib.gdelta_workspace_bytes(d) if train or d.seqlen > 16 else 0,
+        self.workspace = torch.empty(_lib.gdelta_workspace_bytes(d) if train or d.seqlen > _lib.GDELTA_STEP_TOKENS else 0,
                                      dtype=torch.uint8, **kw)
         self.saved, self.grads, self._had_h0 = None, {}, False
         if train:

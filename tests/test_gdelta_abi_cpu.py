@@ -2,6 +2,7 @@
 made before any launch, so they are checked without a GPU."""
 import ctypes
 import os
+import re
 
 import pytest
 
@@ -146,3 +147,12 @@ def test_binding_checks(pkg):
         pkg.gdelta_step(d, *cpu.values(), torch.zeros(s["state"]), y=torch.zeros(s["v"]))
     with pytest.raises(TypeError, match="torch.Tensor"):
         pkg.layernorm_fwd(ln(pkg), [1.0], y=torch.zeros(10, 100))
+
+
+def test_step_tokens_is_the_headers(pkg):
+    text = open(os.path.join(os.path.dirname(__file__), "..", "include", "mamba_gdelta.h")).read()
+    assert int(re.search(r"define MAMBA_GDELTA_STEP_TOKENS (\d+)", text).group(1)) == pkg._lib.GDELTA_STEP_TOKENS
+    train = pkg.gdelta_workspace_bytes(gd(pkg, seqlen=9))
+    for seqlen, size in ((8, 0), (9, train)):
+        core = pkg.GatedDeltaCore(gd(pkg, seqlen=seqlen), device="cpu", train=False)
+        assert core.workspace.numel() == size

@@ -103,7 +103,7 @@ def test_many_heads(mscan, shape, act):
 
 
 @pytest.mark.parametrize("act", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("T", [1, 15, 16, 17, 64, 100, 257])
+@pytest.mark.parametrize("T", [1, 8, 9, 15, 16, 17, 64, 100, 257])
 def test_forward_alone(mscan, act, T):
     """Without anything kept: the short sequences' token-by-token kernel and the chunks; h_last over h0."""
     shape = (2, T, 4, 2, 64, 72, act)
@@ -116,7 +116,8 @@ def test_forward_alone(mscan, act, T):
 
 
 @pytest.mark.parametrize("act", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("shape", [(3, 1, 4, 2, 128, 128), (1, 1, 1, 1, 8, 8), (2, 5, 3, 1, 40, 200), (5, 1, 2, 2, 120, 16)],
+@pytest.mark.parametrize("shape", [(3, 1, 4, 2, 128, 128), (1, 1, 1, 1, 8, 8), (2, 5, 3, 1, 40, 200), (5, 1, 2, 2, 120, 16),
+                                   (20, 3, 28, 4, 72, 40), (65, 2, 8, 8, 16, 32), (64, 1, 8, 1, 128, 24)],
                          ids=str)
 def test_step(mscan, shape, act):
     x, ref = make(*shape, act, seed=7)
