@@ -51,7 +51,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kC = 64;          // tokens per chunk
 constexpr int kFrag = 512;      // u16 of one operand fragment: 64 lanes x 8
-constexpr int kRingTiles = 4;   // 16-column tiles of a workgroup that shares its fragments in LDS
+constexpr int kCopyWaves = 4;   // of a workgroup that shares its tiles' fragments in LDS
 
 // per-token scalars of a chunk, per query / key head: k' = k pk is what the products take, k' rk the unit-length key;
 // q' = q pq, and q' rq the unit-length query times the scale

@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(64) gdelta_dscale_kernel(const BwdArgs p) {
 
 // ------------------------------------------------------------------ pass from the last chunk to the first
 // As the forward's pass: a wave holds 16 columns of dS^T and needs nothing of any other, but for the fragments that the
-// tiles of a head share; they come a chunk ahead, to registers, or with many tiles to LDS.  Fragments of a chunk in the
-// shared buffer, in this order (16-bit inputs only):
+// tiles of a head share; they come a chunk ahead, to LDS for 16-bit inputs (two planes of f32 inputs twice are more than
+// it holds: registers).  Fragments of a chunk in the shared buffer, in this order:
 template <int KP>
 struct BwdRing {
   static constexpr int NF = KP / 8, KF = 0, PT = NF, TT = PT + 12, QT = TT + 12, KT = QT + NF, N = KT + NF;
@@ -237,28 +237,28 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
   for (int64_t c = p.d.nc - 1; c >= 0; --c) ch.step(p, w, c, soc, rso, rps, s);
 }
 
-// Four waves with a tile each and four that copy the fragments, as in the forward
-template <Act A, int KP>
-__global__ void __launch_bounds__(512) gdelta_bwd_ring_kernel(const BwdArgs p) {
+// TILES waves with a tile each and four that copy the fragments, as in the forward
+template <Act A, int KP, int TILES>
+__global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_bwd_ring_kernel(const BwdArgs p) {
   using R = BwdRing<KP>;
   constexpr int NF = R::NF;
   __shared__ __attribute__((aligned(16))) uint16_t ring[2][R::N * kFrag];
-  __shared__ __attribute__((aligned(16))) float s[kRingTiles][4][kC];
+  __shared__ __attribute__((aligned(16))) float s[TILES][4][kC];
   static_assert(sizeof(ring) + sizeof(s) <= mscan::kLdsBytes, "LDS");
   const Dims& d = p.d;
   const int wv = wave_id();
-  const PassPlace<A> w(d, kRingTiles, wv & (kRingTiles - 1));
+  const PassPlace<A> w(d, TILES, wv < TILES ? wv : 0);
   const int64_t last = d.nc - 1;
-  if (wv >= kRingTiles) {
-    const int first = wv - kRingTiles;
+  if (wv >= TILES) {
+    const int first = wv - TILES;
     auto copy = [&](int64_t c) {
       uint16_t* dst = ring[c & 1];
       const int64_t gi = (w.bg * d.nc + c) * (NF * kFrag), ci = (w.bh * d.nc + c) * (12 * kFrag);
-      copy_frags<NF, kRingTiles>(dst + R::KF * kFrag, p.w.KF + gi, first, w.lane);
-      copy_frags<12, kRingTiles>(dst + R::PT * kFrag, p.w.PT + ci, first, w.lane);
-      copy_frags<12, kRingTiles>(dst + R::TT * kFrag, p.w.TT + ci, first, w.lane);
-      copy_frags<NF, kRingTiles>(dst + R::QT * kFrag, p.w.QT + gi, first, w.lane);
-      copy_frags<NF, kRingTiles>(dst + R::KT * kFrag, p.w.KT + gi, first, w.lane);
+      copy_frags<NF, kCopyWaves>(dst + R::KF * kFrag, p.w.KF + gi, first, w.lane);
+      copy_frags<12, kCopyWaves>(dst + R::PT * kFrag, p.w.PT + ci, first, w.lane);
+      copy_frags<12, kCopyWaves>(dst + R::TT * kFrag, p.w.TT + ci, first, w.lane);
+      copy_frags<NF, kCopyWaves>(dst + R::QT * kFrag, p.w.QT + gi, first, w.lane);
+      copy_frags<NF, kCopyWaves>(dst + R::KT * kFrag, p.w.KT + gi, first, w.lane);
       wait_copies();
     };
     copy(last);
@@ -826,10 +826,13 @@ hipError_t launch(const BwdArgs& a, hipStream_t st) {
   hipLaunchKernelGGL(gdelta_dscale_kernel, dim3(bh), dim3(64), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const unsigned tiles = d.VP / 16;
-  if (A == Act::F32 || bh * tiles <= kPairTiles) {
+  if constexpr (A == Act::F32) {   // two planes a family: a chunk's fragments twice are more than the LDS
     hipLaunchKernelGGL((gdelta_bwd_state_kernel<A, KP>), dim3(bh * tiles), dim3(64), 0, st, a);
-  } else if constexpr (A != Act::F32) {
-    hipLaunchKernelGGL((gdelta_bwd_ring_kernel<A, KP>), dim3(bh * ((tiles + kRingTiles - 1) / kRingTiles)), dim3(512), 0, st, a);
+  } else {
+    ring_tiles<true>(bh, tiles, [&](auto n, unsigned grid) {
+      constexpr int N = decltype(n)::value;
+      hipLaunchKernelGGL((gdelta_bwd_ring_kernel<A, KP, N>), dim3(grid), dim3(64 * (N + kCopyWaves)), 0, st, a);
+    });
   }
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const dim3 grid(static_cast<unsigned>(d.B * d.G) * nc);

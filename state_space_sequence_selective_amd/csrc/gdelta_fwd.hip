@@ -653,29 +653,29 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
   }
 }
 
-// The same for many tiles: four waves with a tile of one head each, and four that copy the chunk's fragments into LDS
+// The same for many tiles: TILES waves with a tile of one head each, and four that copy the chunk's fragments into LDS
 // (66 KB for d_k = 128 and bf16, twice) a chunk ahead.  A CU takes about 12 bytes a clock from L2 here, so what bounds
 // the kernel above, once it has several waves a CU, is every wave loading its own copy.
-template <Act A, int KP, bool SAVE>
-__global__ void __launch_bounds__(512) gdelta_fwd_ring_kernel(const FwdArgs p) {
+template <Act A, int KP, bool SAVE, int TILES>
+__global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_fwd_ring_kernel(const FwdArgs p) {
   using R = FwdRing<A, KP>;
   constexpr int NF = R::NF;
   __shared__ __attribute__((aligned(16))) uint16_t ring[2][R::N * kFrag];
-  __shared__ __attribute__((aligned(16))) float s[kRingTiles][4][kC];
+  __shared__ __attribute__((aligned(16))) float s[TILES][4][kC];
   static_assert(sizeof(ring) + sizeof(s) <= mscan::kLdsBytes, "LDS");
   const Dims& d = p.d;
   const int wv = wave_id();
-  const PassPlace<A> w(d, kRingTiles, wv & (kRingTiles - 1));
-  if (wv >= kRingTiles) {
-    const int first = wv - kRingTiles;
+  const PassPlace<A> w(d, TILES, wv < TILES ? wv : 0);
+  if (wv >= TILES) {
+    const int first = wv - TILES;
     auto copy = [&](int64_t c) {
       uint16_t* dst = ring[c & 1];
       const int64_t gi = w.bg * d.nc + c, ci = w.bh * d.nc + c;
-      copy_frags<NF, kRingTiles>(dst + R::KF * kFrag, p.w.KF + gi * (NF * kFrag), first, w.lane);
-      copy_frags<NF, kRingTiles>(dst + R::QF * kFrag, p.w.QF + gi * (NF * kFrag), first, w.lane);
-      copy_frags<12, kRingTiles>(dst + R::T * kFrag, p.w.T + ci * (12 * kFrag), first, w.lane);
-      copy_frags<NF, kRingTiles>(dst + R::KT * kFrag, p.w.KT + gi * (NF * kFrag), first, w.lane);
-      copy_frags<6 * kPPlanes<A>, kRingTiles>(dst + R::P * kFrag, p.w.P + ci * (6 * kPPlanes<A> * kFrag), first, w.lane);
+      copy_frags<NF, kCopyWaves>(dst + R::KF * kFrag, p.w.KF + gi * (NF * kFrag), first, w.lane);
+      copy_frags<NF, kCopyWaves>(dst + R::QF * kFrag, p.w.QF + gi * (NF * kFrag), first, w.lane);
+      copy_frags<12, kCopyWaves>(dst + R::T * kFrag, p.w.T + ci * (12 * kFrag), first, w.lane);
+      copy_frags<NF, kCopyWaves>(dst + R::KT * kFrag, p.w.KT + gi * (NF * kFrag), first, w.lane);
+      copy_frags<6 * kPPlanes<A>, kCopyWaves>(dst + R::P * kFrag, p.w.P + ci * (6 * kPPlanes<A> * kFrag), first, w.lane);
       wait_copies();
     };
     copy(0);
@@ -841,16 +841,18 @@ hipError_t launch_chunks(const FwdArgs& a, bool save, hipStream_t st) {
   hipLaunchKernelGGL((gdelta_prep_kernel<A, KP>), dim3(bh * nc), dim3(256), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const unsigned tiles = bh * (d.VP / 16);
-  if (tiles <= kPairTiles) {
+  if (tiles <= (save ? kPairTilesSave : kPairTiles)) {
     if (save) hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, true, true>), dim3(tiles), dim3(128), 0, st, a);
     else hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, false, true>), dim3(tiles), dim3(128), 0, st, a);
   } else if constexpr (A == Act::F32) {   // two planes a family: a chunk's fragments twice are more than the LDS
     if (save) hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, true, false>), dim3(tiles), dim3(64), 0, st, a);
     else hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, false, false>), dim3(tiles), dim3(64), 0, st, a);
   } else {
-    const dim3 grid(bh * ((d.VP / 16 + kRingTiles - 1) / kRingTiles));
-    if (save) hipLaunchKernelGGL((gdelta_fwd_ring_kernel<A, KP, true>), grid, dim3(512), 0, st, a);
-    else hipLaunchKernelGGL((gdelta_fwd_ring_kernel<A, KP, false>), grid, dim3(512), 0, st, a);
+    ring_tiles<false>(bh, d.VP / 16, [&](auto n, unsigned grid) {
+      constexpr int N = decltype(n)::value;
+      if (save) hipLaunchKernelGGL((gdelta_fwd_ring_kernel<A, KP, true, N>), dim3(grid), dim3(64 * (N + kCopyWaves)), 0, st, a);
+      else hipLaunchKernelGGL((gdelta_fwd_ring_kernel<A, KP, false, N>), dim3(grid), dim3(64 * (N + kCopyWaves)), 0, st, a);
+    });
   }
   return hipGetLastError();
 }

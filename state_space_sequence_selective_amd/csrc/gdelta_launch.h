@@ -1,13 +1,32 @@
 // Host-side launches of the gated delta rule's kernels.
 #pragma once
 
+#include <type_traits>
+
 #include "gdelta.h"
 
 namespace gdelta {
 
-// Up to this many 16-column tiles the passes over the chunks give two waves to each: 1024 SIMDs hold one wave of theirs
-// each (over 256 registers), so more tiles than 512 would wait for others to end.
-constexpr unsigned kPairTiles = 512;
+// How the forward pass over the chunks has its 16-column tiles: up to kPairTiles of them (kPairTilesSave with what a backward
+// pass reads) each has two waves of its own; more share their chunks' fragments in LDS.  Forwards of 2048 tokens, 128 x
+// 128, bf16: 155 us against 186 at 64 heads (512 tiles), 249 against 217 at 80; training passes 318 against 330 at 32
+// heads (256 tiles), 408 and 403 at 40, 574 and 558 at 64.
+constexpr unsigned kPairTiles = 512, kPairTilesSave = 256;
+
+// Tiles of a workgroup that shares its fragments in LDS (it fills a CU): 3 where that takes no more rounds over the 256 CUs
+// than 4, and one (ONE) while there is a CU for each.  The forward pass of 80 heads of 8 tiles takes 603 us with 3 and 678
+// with 4, the reverse pass 624 and 670; a training pass of 2048 tokens 1089 with 3 and 896 with 4 at 128 heads, 316 with
+// one tile and 326 with 3 at 32, 487 and 409 at 40.  With 2 it was within 2 % of 3, with 8 slower than 4 at every count of
+// heads.  launch(integral_constant, grid).
+template <bool ONE, class Launch>
+void ring_tiles(unsigned heads, unsigned tiles, Launch launch) {
+  const unsigned g3 = heads * ((tiles + 2) / 3), g4 = heads * ((tiles + 3) / 4);
+  if constexpr (ONE) {
+    if (heads * tiles <= 256) return launch(std::integral_constant<int, 1>{}, heads * tiles);
+  }
+  if ((g3 + 255) / 256 <= (g4 + 255) / 256) launch(std::integral_constant<int, 3>{}, g3);
+  else launch(std::integral_constant<int, 4>{}, g4);
+}
 
 // Chunked forward; `save`: also what the backward pass reads.
 hipError_t launch_fwd(Act act, const FwdArgs& a, bool save, hipStream_t st);

@@ -90,10 +90,11 @@ def test_forward_and_backward(mscan, shape, act, h0):
 
 
 @pytest.mark.parametrize("act", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("shape", [(6, 70, 24, 24, 40, 80), (9, 130, 16, 8, 120, 64)], ids=str)
+@pytest.mark.parametrize("shape", [(6, 70, 24, 24, 40, 80), (9, 130, 16, 8, 120, 64), (4, 70, 20, 5, 72, 64),
+                                   (3, 65, 30, 30, 64, 104)], ids=str)
 def test_many_heads(mscan, shape, act):
-    """More 16-column tiles than waves: the passes that share a head's operands (a workgroup of the first shape has tiles
-    behind the columns)."""
+    """More 16-column tiles than waves: the passes that share a head's operands, three and four tiles to a workgroup, some
+    with tiles behind the columns."""
     x, ref = make(*shape, act, seed=29)
     train(mscan, (*shape, act), x, ref, h0=True)
     core = mscan.GatedDeltaCore(dims_of(mscan, *shape, act), train=False)
