@@ -49,9 +49,9 @@ extern "C" {
 #endif
 
 typedef struct {
-  int64_t batch;   /* >= 1 */
+  int64_t batch;   /* >= 1; batch * heads * max(seqlen / 64, d_v / 32) below 2^23 */
   int64_t seqlen;  /* 1 .. 2^24 */
-  int64_t heads;   /* >= 1, a multiple of groups */
+  int64_t heads;   /* >= 1, a multiple of groups; heads * d_v and groups * d_k below 2^23 */
   int64_t groups;  /* >= 1: query / key heads */
   int64_t d_k;     /* 8 .. 128, a multiple of 8 */
   int64_t d_v;     /* 8 .. 512, a multiple of 8 */

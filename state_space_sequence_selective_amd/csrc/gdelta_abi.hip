@@ -43,8 +43,8 @@ int check_dims(const mamba_gdelta_dims_t* dd, Dims* d, Act* act) {
   if (dd->heads * dd->d_v >= (int64_t(1) << 23) || dd->groups * dd->d_k >= (int64_t(1) << 23))   // 64 rows in 32-bit bytes
     return fail(MAMBA_ERR_CAPACITY, "heads * d_v and groups * d_k must be below 2^23");
   const int64_t nc = (dd->seqlen + kC - 1) / kC, per = (dd->d_v + 31) / 32;
-  if (dd->batch * dd->heads * (nc > per ? nc : per) >= (int64_t(1) << 24))   // workgroups of 256: fewer than 2^32 threads
-    return fail(MAMBA_ERR_CAPACITY, "batch * heads * max(seqlen / 64, d_v / 32) must be below 2^24");
+  if (dd->batch * dd->heads * (nc > per ? nc : per) >= (int64_t(1) << 23))   // workgroups of at most 512: fewer than 2^32 threads
+    return fail(MAMBA_ERR_CAPACITY, "batch * heads * max(seqlen / 64, d_v / 32) must be below 2^23");
   d->B = dd->batch;
   d->T = dd->seqlen;
   d->H = dd->heads;
