@@ -27,12 +27,16 @@ __global__ void __launch_bounds__(256) gdelta_dymax_kernel(const BwdArgs p) {
   const int64_t c = at_.c, h = at_.h, b = at_.b, bh = b * d.H + h;
   const int64_t t0 = c * kC, left = d.T - t0;
   float m = 0.0f;
-  const int row = tid >> 2;   // four threads a row, four loads in flight
-  for (int c0 = (tid & 3) * 8; c0 < d.V; c0 += 4 * 32) {
+  // the chunk's 16-byte pieces (of bf16) in order, four loads in flight a thread; i / n by a factor exact for i < 64 n, n <= 64
+  const uint32_t n = static_cast<uint32_t>(d.V / 8), inv = (1u << 20) / n + 1;
+  const uint32_t end = static_cast<uint32_t>(left < kC ? left : kC) * n;
+  for (uint32_t i0 = tid; i0 < end; i0 += 4 * 256) {
     float x[4][8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      load8<A>(p.dy, ((b * d.T + t0 + row) * d.H + h) * d.V + c0 + 32 * k, row < left && c0 + 32 * k < d.V, x[k]);
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint32_t i = i0 + 256 * k, row = i * inv >> 20;
+      load8<A>(p.dy, ((b * d.T + t0 + row) * d.H + h) * d.V + (i - row * n) * 8, i < end, x[k]);
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
