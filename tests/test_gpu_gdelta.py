@@ -78,7 +78,8 @@ def train(mscan, shape, x, ref, h0=None, **kw):
 
 # B, T, H, G, d_k, d_v
 SHAPES = [(1, 64, 1, 1, 64, 32), (2, 65, 2, 1, 64, 64), (1, 63, 4, 2, 32, 48), (1, 130, 3, 3, 128, 128),
-          (2, 17, 4, 1, 8, 8), (1, 200, 2, 2, 72, 40), (1, 129, 2, 1, 128, 136), (1, 1, 2, 2, 64, 64), (3, 2, 2, 1, 16, 24)]
+          (2, 17, 4, 1, 8, 8), (1, 200, 2, 2, 72, 40), (1, 129, 2, 1, 128, 136), (1, 1, 2, 2, 64, 64), (3, 2, 2, 1, 16, 24),
+          (1, 70, 4, 2, 128, 512), (2, 65, 1, 1, 8, 264)]
 
 
 @pytest.mark.parametrize("act", ["f32", "bf16", "f16"])
@@ -280,3 +281,49 @@ def test_a_nan_stays_in_its_heads_and_batch_rows(mscan):
     assert torch.equal(y[1], clean[1]) and torch.equal(y[0, :, [0, 2, 3]], clean[0, :, [0, 2, 3]])
     assert torch.equal(y[0, :64, 1], clean[0, :64, 1])
     assert bool(torch.isnan(y[0, 70:, 1]).all())
+
+
+@pytest.mark.parametrize("shape", [(2, 1, 4, 2, 64, 64, "bf16"), (20, 1, 28, 4, 72, 40, "f16")], ids=str)
+def test_decoding_replayed_on_a_stream(mscan, shape):
+    """A decoding step captured on a side stream: each replay takes the next token and the state the last one left."""
+    xs = [make(*shape, seed=s)[0] for s in (1, 2, 3, 4)]
+    live = {n: t.clone() for n, t in xs[0].items()}
+    d = dims_of(mscan, *shape)
+    eager, core = mscan.GatedDeltaCore(d, train=False), mscan.GatedDeltaCore(d, train=False)
+    state, want = xs[0]["h0"].clone(), xs[0]["h0"].clone()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        core.step(live, state)
+    for x in xs + xs[:1]:
+        for n in live:
+            live[n].copy_(x[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        y = eager.step(x, want)
+        torch.cuda.synchronize()
+        assert torch.equal(core.y, y) and torch.equal(state, want)
+
+
+def test_two_streams_at_once(mscan):
+    """Two cores with buffers of their own, on two streams at the same time: each as alone."""
+    shape = (2, 200, 8, 4, 64, 64, "bf16")
+    d = dims_of(mscan, *shape)
+    xs = [make(*shape, seed=s)[0] for s in (5, 6)]
+    cores, streams = [mscan.GatedDeltaCore(d) for _ in xs], [torch.cuda.Stream() for _ in xs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for x, core, s in zip(xs, cores, streams):
+            with torch.cuda.stream(s):
+                core.zero_grads()
+                core.forward(x)
+                core.backward(x, x["dy"])
+    torch.cuda.synchronize()
+    for x, core in zip(xs, cores):
+        alone = mscan.GatedDeltaCore(d)
+        alone.forward(x)
+        alone.backward(x, x["dy"])
+        torch.cuda.synchronize()
+        assert torch.equal(core.y, alone.y) and all(torch.equal(core.grads[n], alone.grads[n]) for n in NAMES)
