@@ -221,6 +221,19 @@ __device__ __forceinline__ void store_packed(uint32_t* base, int off, const Frag
 
 __device__ __forceinline__ h8 ld8(const uint16_t* p) { return *reinterpret_cast<const h8*>(p); }
 
+// A fragment of a family's transpose out of the family's own fragments in LDS ([4 token tiles][KP / 32 steps of d_k]):
+// ds_read_b64_tr_b16 takes four rows of 16 elements, 8 bytes a lane, and gives lane i their column i.  Here a row is a
+// token's 16 d_k of tile mt, four lanes' pieces in a fragment.  f: the family + trans_lane(); i: 2 mt + step of 32 tokens.
+__device__ __forceinline__ int trans_lane(int lane) { return ((lane & 3) * 16 + (lane >> 2)) * 8; }
+template <int KP>
+__device__ __forceinline__ h8 ld_trans(const uint16_t* f, int i) {
+  typedef short s4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s4 lds_s4;
+  const uint16_t* a = f + (2 * (i & 1) * (KP / 32) + (i >> 2)) * kFrag + ((i >> 1) & 1) * 4;
+  const s4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)a), y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(a + KP / 32 * kFrag));
+  return __builtin_bit_cast(h8, (short __attribute__((ext_vector_type(8)))){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+}
+
 __device__ __forceinline__ float max_finite(float m, float x) {
   const float a = fabsf(x);
   return a < 3.0e38f ? fmaxf(m, a) : m;   // false for NaN too

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(64) gdelta_dscale_kernel(const BwdArgs p) {
 // it holds: registers).  Fragments of a chunk in the shared buffer, in this order:
 template <int KP>
 struct BwdRing {
-  static constexpr int NF = KP / 8, KF = 0, PT = NF, TT = PT + 12, QT = TT + 12, KT = QT + NF, N = KT + NF;
+  static constexpr int NF = KP / 8, KF = 0, PT = NF, TT = PT + 12, QF = TT + 12, N = QF + NF;
 };
 
 template <Act A, int KP, bool RING>
@@ -90,11 +90,16 @@ struct BackChain {
   h8 kf[RING ? 1 : NF], kt[RING ? 1 : NF], qt[RING ? 1 : NF], ph[RING ? 1 : 6], pl[RING ? 1 : 6], th[RING ? 1 : 6], tl[RING ? 1 : 6];
   float sc[4], el;
   uint32_t v[4][4];
-  const uint16_t* ring;   // + this lane's place
+  const uint16_t *ring, *ring_t;   // + this lane's place, plain and for a transpose
 
   template <int N>
   __device__ __forceinline__ h8 get(const h8 (&x)[N], int base, int i) const {
     if constexpr (RING) return ld8(ring + (base + i) * kFrag);
+    else return x[i];
+  }
+  template <int N>
+  __device__ __forceinline__ h8 get_t(const h8 (&x)[N], int base, int i) const {
+    if constexpr (RING) return ld_trans<KP>(ring_t + base * kFrag, i);
     else return x[i];
   }
   template <int N>
@@ -197,7 +202,7 @@ struct BackChain {
     const Frag e0 = to_b(dO[0], dO[1]), e1 = to_b(dO[2], dO[3]);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) dS[mt] *= elc;
-    update(qt, R::QT, QT + group(w, c), e0, e1, w.lane);
+    update(qt, R::QF, QT + group(w, c), e0, e1, w.lane);
     load(qt, QT + group(w, next), w.lane);
     store_packed(p.DU + ci * kC * VP, poff, to_b(Y[0], Y[1]), VP);
     store_packed(p.DU + (ci * kC + 32) * VP, poff, to_b(Y[2], Y[3]), VP);
@@ -207,7 +212,7 @@ struct BackChain {
       dv[mt] = Y[mt] * *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * w.g) * rso;
       Y[mt] *= -*reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * w.g);
     }
-    update(kt, R::KT, KT + group(w, c), to_b(Y[0], Y[1]), to_b(Y[2], Y[3]), w.lane);
+    update(kt, R::KF, KT + group(w, c), to_b(Y[0], Y[1]), to_b(Y[2], Y[3]), w.lane);
     load(kt, KT + group(w, next), w.lane);
     store_cols<A>(dv, static_cast<char*>(p.d_v) + w.at_chunk(c), w.row, w.col * Place::ES, w.T - c * kC, w.g, w.ok);
   }
@@ -215,13 +220,13 @@ struct BackChain {
   template <int N>
   __device__ __forceinline__ void update(const h8 (&x)[N], int base, const uint16_t* global, const Frag& a, const Frag& b, int lane) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get(x, base, 2 * mt), a.hi, dS[mt]);
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get_t(x, base, 2 * mt), a.hi, dS[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get(x, base, 2 * mt), a.lo, dS[mt]);
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get_t(x, base, 2 * mt), a.lo, dS[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get(x, base, 2 * mt + 1), b.hi, dS[mt]);
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get_t(x, base, 2 * mt + 1), b.hi, dS[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get(x, base, 2 * mt + 1), b.lo, dS[mt]);
+    for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get_t(x, base, 2 * mt + 1), b.lo, dS[mt]);
     if (NP == 2) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -243,8 +248,8 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
 }
 
 // TILES waves with a tile each and four that copy the fragments, as in the forward and bound by the same: 8192 tokens of 80
-// heads of 128 x 128 take 610 us, 2.1 GB of HBM traffic at 3.4 TB/s, against 850 with the fragments in each wave's
-// registers; 2048 tokens of 96 heads of 64 x 64 take 91 against 124.
+// heads of 128 x 128 take 610 us, 2 GB of HBM traffic at 3.3 TB/s, against 850 with the fragments in each wave's
+// registers; 2048 tokens of 96 heads of 64 x 64 take 87 against 124.
 template <Act A, int KP, int TILES>
 __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_bwd_ring_kernel(const BwdArgs p) {
   using R = BwdRing<KP>;
@@ -264,8 +269,7 @@ __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_bwd_ring_ker
       copy_frags<NF, kCopyWaves>(dst + R::KF * kFrag, p.w.KF + gi, first, w.lane);
       copy_frags<12, kCopyWaves>(dst + R::PT * kFrag, p.w.PT + ci, first, w.lane);
       copy_frags<12, kCopyWaves>(dst + R::TT * kFrag, p.w.TT + ci, first, w.lane);
-      copy_frags<NF, kCopyWaves>(dst + R::QT * kFrag, p.w.QT + gi, first, w.lane);
-      copy_frags<NF, kCopyWaves>(dst + R::KT * kFrag, p.w.KT + gi, first, w.lane);
+      copy_frags<NF, kCopyWaves>(dst + R::QF * kFrag, p.w.QF + gi, first, w.lane);
       wait_copies();
     };
     copy(last);
@@ -284,6 +288,7 @@ __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_bwd_ring_ker
   for (int64_t c = last; c >= 0; --c) {
     if (live) {
       ch.ring = ring[c & 1] + w.lane * 8;
+      ch.ring_t = ring[c & 1] + trans_lane(w.lane);
       ch.step(p, w, c, soc, rso, rps, s[wv]);
     }
     mscan::lds_barrier();

@@ -373,7 +373,7 @@ struct PassBuf {
 // Fragments of a chunk in a shared buffer, in this order; 16-bit inputs only
 template <Act A, int KP>
 struct FwdRing {
-  static constexpr int NF = KP / 8, KF = 0, QF = NF, T = 2 * NF, KT = T + 12, P = KT + NF, N = P + 6 * kPPlanes<A>;
+  static constexpr int NF = KP / 8, KF = 0, QF = NF, T = 2 * NF, P = T + 12, N = P + 6 * kPPlanes<A>;
 };
 
 // RING: fragments come from the shared buffer instead of registers
@@ -386,12 +386,16 @@ struct Chain {
   h8 kf[RING ? 1 : NF], kt[RING ? 1 : NF], th[RING ? 1 : 6], tl[RING ? 1 : 6];
   float sc[3], el;
   uint32_t v[4][4];
-  const uint16_t* ring;   // + this lane's place
+  const uint16_t *ring, *ring_t;   // + this lane's place, plain and for a transpose
 
   template <int N>
   __device__ __forceinline__ h8 get(const h8 (&x)[N], int base, int i) const {
     if constexpr (RING) return ld8(ring + (base + i) * kFrag);
     else return x[i];
+  }
+  __device__ __forceinline__ h8 get_kt(int i) const {
+    if constexpr (RING) return ld_trans<KP>(ring_t + R::KF * kFrag, i);
+    else return kt[i];
   }
   template <int N>
   __device__ __forceinline__ void load(h8 (&x)[N], const uint16_t* base, int lane) {
@@ -478,13 +482,13 @@ struct Chain {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) S[mt] *= elc;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get(kt, R::KT, 2 * mt), d0.hi, S[mt]);
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get_kt(2 * mt), d0.hi, S[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get(kt, R::KT, 2 * mt), d0.lo, S[mt]);
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get_kt(2 * mt), d0.lo, S[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get(kt, R::KT, 2 * mt + 1), d1.hi, S[mt]);
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get_kt(2 * mt + 1), d1.hi, S[mt]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get(kt, R::KT, 2 * mt + 1), d1.lo, S[mt]);
+    for (int mt = 0; mt < MT; ++mt) S[mt] = mma(get_kt(2 * mt + 1), d1.lo, S[mt]);
     if (NP == 2) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -657,10 +661,11 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
 }
 
 // The same for many tiles: TILES waves with a tile of one head each, and four that copy the chunk's fragments into LDS
-// (66 KB for d_k = 128 and bf16, twice) a chunk ahead.  What bounds the kernel above, once it has several waves a CU, is
+// (50 KB for d_k = 128 and bf16, twice) a chunk ahead.  What bounds the kernel above, once it has several waves a CU, is
 // every wave loading its own copy (12 bytes a clock and CU); this one the CU's path to memory, copies in and the parts of S
-// and u out: 8192 tokens of 80 heads of 128 x 128 take 600 us, 2.05 GB of HBM traffic at 3.4 TB/s (the copies alone 250,
-// the products alone 276), against 850 without sharing.
+// and u out: 8192 tokens of 80 heads of 128 x 128 take 564 us, 2 GB of HBM traffic at 3.5 TB/s (the products alone 276),
+// against 850 without sharing.  k's transpose is read out of k, which leaves a family less to copy (602 -> 564 us; 96 heads
+// of 64 x 64 take 109 either way).
 template <Act A, int KP, bool SAVE, int TILES>
 __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_fwd_ring_kernel(const FwdArgs p) {
   using R = FwdRing<A, KP>;
@@ -679,7 +684,6 @@ __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_fwd_ring_ker
       copy_frags<NF, kCopyWaves>(dst + R::KF * kFrag, p.w.KF + gi * (NF * kFrag), first, w.lane);
       copy_frags<NF, kCopyWaves>(dst + R::QF * kFrag, p.w.QF + gi * (NF * kFrag), first, w.lane);
       copy_frags<12, kCopyWaves>(dst + R::T * kFrag, p.w.T + ci * (12 * kFrag), first, w.lane);
-      copy_frags<NF, kCopyWaves>(dst + R::KT * kFrag, p.w.KT + gi * (NF * kFrag), first, w.lane);
       copy_frags<6 * kPPlanes<A>, kCopyWaves>(dst + R::P * kFrag, p.w.P + ci * (6 * kPPlanes<A> * kFrag), first, w.lane);
       wait_copies();
     };
@@ -705,6 +709,7 @@ __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_fwd_ring_ker
   for (int64_t c = 0; c < d.nc; ++c) {
     if (live) {
       ch.ring = out.ring = ring[c & 1] + w.lane * 8;
+      ch.ring_t = ring[c & 1] + trans_lane(w.lane);
       out.begin(w, s[wv][3]);
       ch.step(p, w, c, sv, s[wv], [&](int ks, const Frag& f) { out.state(p, w, c, ks, f); },
               [&](const Frag& u0, const Frag& u1) { out.u(p, w, c, yscale, s[wv][3], u0, u1); });
