@@ -225,13 +225,35 @@ __device__ __forceinline__ h8 ld8(const uint16_t* p) { return *reinterpret_cast<
 // ds_read_b64_tr_b16 takes four rows of 16 elements, 8 bytes a lane, and gives lane i their column i.  Here a row is a
 // token's 16 d_k of tile mt, four lanes' pieces in a fragment.  f: the family + trans_lane(); i: 2 mt + step of 32 tokens.
 __device__ __forceinline__ int trans_lane(int lane) { return ((lane & 3) * 16 + (lane >> 2)) * 8; }
+__device__ __forceinline__ u32x2 read_trans(const uint16_t* a) {
+  typedef short s4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)a));
+}
 template <int KP>
 __device__ __forceinline__ h8 ld_trans(const uint16_t* f, int i) {
-  typedef short s4 __attribute__((ext_vector_type(4)));
-  typedef __attribute__((address_space(3))) s4 lds_s4;
   const uint16_t* a = f + (2 * (i & 1) * (KP / 32) + (i >> 2)) * kFrag + ((i >> 1) & 1) * 4;
-  const s4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)a), y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(a + KP / 32 * kFrag));
-  return __builtin_bit_cast(h8, (short __attribute__((ext_vector_type(8)))){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+  const u32x2 x = read_trans(a), y = read_trans(a + KP / 32 * kFrag);
+  return __builtin_bit_cast(h8, (u32x4{x[0], x[1], y[0], y[1]}));
+}
+
+// The same from the parts in LDS (their 64 x 16 bytes each, high then low: keep_parts), read transposed so that a lane has
+// four columns of a row: two stores of 16 bytes a lane in place of eight of 4.  base: the tile's first column; off:
+// store_off().
+__device__ __forceinline__ void keep_parts(uint16_t* lds, int lane, const Frag& f) {
+  *reinterpret_cast<h8*>(lds + lane * 8) = f.hi;
+  *reinterpret_cast<h8*>(lds + kFrag + lane * 8) = f.lo;
+}
+__device__ __forceinline__ int store_off(int lane, int words) { return ((lane & 15) * words + (lane >> 4) * 4) * 4; }
+__device__ __forceinline__ void store_kept(uint32_t* base, int off, const uint16_t* lds, int lane, int words) {
+  const Buf b = buf_of(base);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint16_t* a = lds + trans_lane(lane) + 4 * half;
+    const u32x2 hi = read_trans(a), lo = read_trans(a + kFrag);
+    const u32x4 x = {__builtin_amdgcn_perm(lo[0], hi[0], 0x05040100), __builtin_amdgcn_perm(lo[0], hi[0], 0x07060302),
+                     __builtin_amdgcn_perm(lo[1], hi[1], 0x05040100), __builtin_amdgcn_perm(lo[1], hi[1], 0x07060302)};
+    __builtin_amdgcn_raw_buffer_store_b128(x, b, off, 16 * half * words * 4, 0);
+  }
 }
 
 __device__ __forceinline__ float max_finite(float m, float x) {

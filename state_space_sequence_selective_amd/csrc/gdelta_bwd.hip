@@ -91,6 +91,10 @@ struct BackChain {
   float sc[4], el;
   uint32_t v[4][4];
   const uint16_t *ring, *ring_t;   // + this lane's place, plain and for a transpose
+  // the parts of dS and Y through LDS to wide stores: 563 us against 603 for 8192 tokens of 80 heads of 128 x 128, 89
+  // against 87 for 2048 tokens of 96 heads of 64 x 64
+  static constexpr bool KEEP = RING && KP == 128;
+  uint16_t* kept;   // [KS][high, low] fragments of the wave's own
 
   template <int N>
   __device__ __forceinline__ h8 get(const h8 (&x)[N], int base, int i) const {
@@ -157,7 +161,8 @@ struct BackChain {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const Frag f = to_b(dS[2 * ks], dS[2 * ks + 1]);
-      store_packed(p.DS + (ci * KP + 32 * ks) * VP, poff, f, VP);
+      if constexpr (KEEP) keep_parts(kept + 2 * ks * kFrag, w.lane, f);
+      else store_packed(p.DS + (ci * KP + 32 * ks) * VP, poff, f, VP);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(get(kf, R::KF, mt * KS + ks), f.hi, dU[mt]);
 #pragma unroll
@@ -204,8 +209,22 @@ struct BackChain {
     for (int mt = 0; mt < MT; ++mt) dS[mt] *= elc;
     update(qt, R::QF, QT + group(w, c), e0, e1, w.lane);
     load(qt, QT + group(w, next), w.lane);
-    store_packed(p.DU + ci * kC * VP, poff, to_b(Y[0], Y[1]), VP);
-    store_packed(p.DU + (ci * kC + 32) * VP, poff, to_b(Y[2], Y[3]), VP);
+    if constexpr (KEEP) {
+      const int off = store_off(w.lane, VP), v0 = w.col - w.r;
+      mscan::wave_lds_sync();
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) store_kept(p.DS + (ci * KP + 32 * ks) * VP + v0, off, kept + 2 * ks * kFrag, w.lane, VP);
+      mscan::wave_lds_sync();
+      keep_parts(kept, w.lane, to_b(Y[0], Y[1]));
+      keep_parts(kept + 2 * kFrag, w.lane, to_b(Y[2], Y[3]));
+      mscan::wave_lds_sync();
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) store_kept(p.DU + (ci * kC + 32 * ks) * VP + v0, off, kept + 2 * ks * kFrag, w.lane, VP);
+      mscan::wave_lds_sync();
+    } else {
+      store_packed(p.DU + ci * kC * VP, poff, to_b(Y[0], Y[1]), VP);
+      store_packed(p.DU + (ci * kC + 32) * VP, poff, to_b(Y[2], Y[3]), VP);
+    }
     f32x4 dv[4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
@@ -248,7 +267,7 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
 }
 
 // TILES waves with a tile each and four that copy the fragments, as in the forward and bound by the same: 8192 tokens of 80
-// heads of 128 x 128 take 610 us, 2 GB of HBM traffic at 3.3 TB/s, against 850 with the fragments in each wave's
+// heads of 128 x 128 take 563 us, 2 GB of HBM traffic at 3.5 TB/s, against 850 with the fragments in each wave's
 // registers; 2048 tokens of 96 heads of 64 x 64 take 87 against 124.
 template <Act A, int KP, int TILES>
 __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_bwd_ring_kernel(const BwdArgs p) {
@@ -256,7 +275,8 @@ __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_bwd_ring_ker
   constexpr int NF = R::NF;
   __shared__ __attribute__((aligned(16))) uint16_t ring[2][R::N * kFrag];
   __shared__ __attribute__((aligned(16))) float s[TILES][4][kC];
-  static_assert(sizeof(ring) + sizeof(s) <= mscan::kLdsBytes, "LDS");
+  __shared__ __attribute__((aligned(16))) uint16_t kept[TILES][BackChain<A, KP, true>::KEEP ? KP / 16 * kFrag : 1];
+  static_assert(sizeof(ring) + sizeof(s) + sizeof(kept) <= mscan::kLdsBytes, "LDS");
   const Dims& d = p.d;
   const int wv = wave_id();
   const PassPlace<A> w(d, TILES, wv < TILES ? wv : 0);
@@ -283,6 +303,7 @@ __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_bwd_ring_ker
   const float so = p.so[w.bh], rso = 1.0f / so, rps = 1.0f / d.pscale, soc = w.ok ? so : 0.0f;
   const bool live = w.col < d.VP;   // a head's last workgroup may have tiles behind its columns
   BackChain<A, KP, true> ch;
+  ch.kept = kept[wv];
   if (live) ch.init(p, w);
   mscan::lds_barrier();
   for (int64_t c = last; c >= 0; --c) {

@@ -518,6 +518,10 @@ struct Output {
   float eq;
   f32x4 y[4];
   const uint16_t* ring;
+  // the parts of S and u through LDS to wide stores: 2048 tokens of 96 heads of 64 x 64 take 94 us against 111; 8192 tokens
+  // of 80 heads of 128 x 128 659 against 561
+  static constexpr bool KEEP = SAVE && RING && KP == 64;
+  uint16_t* kept;   // [KS][high, low] fragments of the wave's own
 
   template <int N>
   __device__ __forceinline__ h8 get(const h8 (&x)[N], int base, int i) const {
@@ -542,7 +546,8 @@ struct Output {
     for (int mt = 0; mt < 4; ++mt) y[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   __device__ __forceinline__ void state(const FwdArgs& p, const Place& w, int64_t c, int ks, const Frag& f) {
-    if (SAVE) store_packed(p.w.S + ((w.bh * w.nc + c) * KP + 32 * ks) * p.d.VP, (4 * w.g * p.d.VP + w.col) * 4, f, p.d.VP);
+    if constexpr (KEEP) keep_parts(kept + 2 * ks * kFrag, w.lane, f);
+    else if (SAVE) store_packed(p.w.S + ((w.bh * w.nc + c) * KP + 32 * ks) * p.d.VP, (4 * w.g * p.d.VP + w.col) * 4, f, p.d.VP);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) y[mt] = mma(get(qf, R::QF, mt * KS + ks), f.hi, y[mt]);
     if (PP == 2) {
@@ -559,7 +564,19 @@ struct Output {
     load_q(p, w, next);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) y[mt] *= *reinterpret_cast<const f32x4*>(s + 16 * mt + 4 * w.g);
-    if (SAVE) {
+    if constexpr (KEEP) {
+      const int off = store_off(w.lane, p.d.VP), v0 = w.col - w.r;
+      mscan::wave_lds_sync();
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) store_kept(p.w.S + (ci * KP + 32 * ks) * p.d.VP + v0, off, kept + 2 * ks * kFrag, w.lane, p.d.VP);
+      mscan::wave_lds_sync();
+      keep_parts(kept, w.lane, u0);
+      keep_parts(kept + 2 * kFrag, w.lane, u1);
+      mscan::wave_lds_sync();
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) store_kept(p.w.U + (ci * kC + 32 * ks) * p.d.VP + v0, off, kept + 2 * ks * kFrag, w.lane, p.d.VP);
+      mscan::wave_lds_sync();
+    } else if (SAVE) {
       const int off = (4 * w.g * p.d.VP + w.col) * 4;
       store_packed(p.w.U + ci * kC * p.d.VP, off, u0, p.d.VP);
       store_packed(p.w.U + (ci * kC + 32) * p.d.VP, off, u1, p.d.VP);
@@ -664,15 +681,15 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
 // (50 KB for d_k = 128 and bf16, twice) a chunk ahead.  What bounds the kernel above, once it has several waves a CU, is
 // every wave loading its own copy (12 bytes a clock and CU); this one the CU's path to memory, copies in and the parts of S
 // and u out: 8192 tokens of 80 heads of 128 x 128 take 564 us, 2 GB of HBM traffic at 3.5 TB/s (the products alone 276),
-// against 850 without sharing.  k's transpose is read out of k, which leaves a family less to copy (602 -> 564 us; 96 heads
-// of 64 x 64 take 109 either way).
+// against 850 without sharing.  k's transpose is read out of k, which leaves a family less to copy (602 -> 564 us).
 template <Act A, int KP, bool SAVE, int TILES>
 __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_fwd_ring_kernel(const FwdArgs p) {
   using R = FwdRing<A, KP>;
   constexpr int NF = R::NF;
   __shared__ __attribute__((aligned(16))) uint16_t ring[2][R::N * kFrag];
   __shared__ __attribute__((aligned(16))) float s[TILES][4][kC];
-  static_assert(sizeof(ring) + sizeof(s) <= mscan::kLdsBytes, "LDS");
+  __shared__ __attribute__((aligned(16))) uint16_t kept[TILES][Output<A, KP, SAVE, true>::KEEP ? KP / 16 * kFrag : 1];
+  static_assert(sizeof(ring) + sizeof(s) + sizeof(kept) <= mscan::kLdsBytes, "LDS");
   const Dims& d = p.d;
   const int wv = wave_id();
   const PassPlace<A> w(d, TILES, wv < TILES ? wv : 0);
@@ -700,6 +717,7 @@ __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_fwd_ring_ker
   if (SAVE && threadIdx.x == 0 && w.col < 16) p.w.sv[w.bh] = sv;
   Chain<A, KP, true> ch;
   Output<A, KP, SAVE, true> out;
+  out.kept = kept[wv];
   const bool live = w.col < d.VP;   // a head's last workgroup may have tiles behind its columns
   if (live) {
     ch.init(p, w, sv);
