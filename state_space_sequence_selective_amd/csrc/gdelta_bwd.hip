@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
 }
 
 // TILES waves with a tile each and four that copy the fragments, as in the forward and bound by the same: 8192 tokens of 80
-// heads of 128 x 128 take 563 us, 2 GB of HBM traffic at 3.5 TB/s, against 850 with the fragments in each wave's
+// heads of 128 x 128 take 570 us, 2 GB of HBM traffic at 3.5 TB/s, against 850 with the fragments in each wave's
 // registers; 2048 tokens of 96 heads of 64 x 64 take 87 against 124.
 template <Act A, int KP, int TILES>
 __global__ void __launch_bounds__(64 * (TILES + kCopyWaves)) gdelta_bwd_ring_kernel(const BwdArgs p) {

@@ -14,8 +14,8 @@ namespace gdelta {
 constexpr unsigned kPairTiles = 512, kPairTilesSave = 256;
 
 // Tiles of a workgroup that shares its fragments in LDS (it fills a CU): 3 where that takes no more rounds over the 256 CUs
-// than 4, and one (ONE) while there is a CU for each.  The forward pass of 80 heads of 8 tiles takes 603 us with 3 and 678
-// with 4, the reverse pass 624 and 670; a training pass of 2048 tokens 1089 with 3 and 896 with 4 at 128 heads, 316 with
+// than 4, and one (ONE) while there is a CU for each.  The forward pass of 80 heads of 8 tiles takes 566 us with 3 and 665
+// with 4, the reverse pass 570 and 689; a training pass of 2048 tokens 1089 with 3 and 896 with 4 at 128 heads, 316 with
 // one tile and 326 with 3 at 32, 487 and 409 at 40.  With 2 it was within 2 % of 3, with 8 slower than 4 at every count of
 // heads.  launch(integral_constant, grid).
 template <bool ONE, class Launch>
