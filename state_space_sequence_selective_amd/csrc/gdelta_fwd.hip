@@ -107,7 +107,8 @@ constexpr int kPPlanes = A == Act::BF16 ? 1 : 2;
 // result tiles of k.q^T and q.k^T as they stand; A = beta k.k^T D in LDS and its unit lower triangular inverse: four
 // 16 x 16 diagonal blocks by substitution, then two levels of T21 = -T22 (A21 T11) on f32 matrix instructions
 // (v_mfma_f32_16x16x4_f32; full f32, as an inverse amplifies roundings of A).  Five workgroups a CU hide the solve's
-// steps (271 -> 250 us), which leaves it to HBM: 8192 tokens of 80 heads of d_k = 128 are 1.33 GB, 5.3 TB/s.
+// steps (271 -> 250 us), which leaves it to HBM: 8192 tokens of 80 heads of d_k = 128 are 1.33 GB, 5.3 TB/s.  f32 rows
+// of 128 need the registers of four (a forward of 4096 tokens of 16 heads 808 -> 613 us).
 constexpr int kAS = kC + 4;
 
 __device__ __forceinline__ f32x4 mma32(float a, float b, f32x4 c) {
@@ -129,7 +130,7 @@ __device__ __forceinline__ f32x4 tile_mm(const float* a, f32x4 b, int r, int g, 
 }
 
 template <Act A, int KP>
-__global__ void __launch_bounds__(256, 5) gdelta_prep_kernel(const FwdArgs p) {
+__global__ void __launch_bounds__(256, A == Act::F32 && KP == 128 ? 4 : 5) gdelta_prep_kernel(const FwdArgs p) {
   constexpr int NP = A == Act::F32 ? 2 : 1, KS = KP / 32, NF = KP / 8;
   __shared__ __attribute__((aligned(16))) float sA[kC * kAS];   // A, and block by block its place taken by T
   __shared__ double sG[kC];
