@@ -206,6 +206,16 @@ __device__ __forceinline__ void wait_copies() {
   __builtin_amdgcn_s_waitcnt(0);
 }
 
+// A family's second plane (f32 inputs) into a wave's own LDS for its next chunk, once its reads of the last one are done;
+// wait_low() ends it.  Loaded where they are used, these planes took 12 to 20 us a chunk of 128 x 128 in place of 4 to 7
+// (4096 tokens of 16 heads: forward 614 -> 259 us).
+template <int N>
+__device__ __forceinline__ void copy_low(uint16_t* dst, const uint16_t* src, int lane) {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  copy_frags<N, 1>(dst, src, 0, lane);
+}
+__device__ __forceinline__ void wait_low() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // Stores a split operand's parts as f16 high | low << 16 words to its 4 + 4 rows 4 g + e, 16 + 4 g + e of `words` words;
 // off: the lane's byte offset in the first of them
 __device__ __forceinline__ void store_packed(uint32_t* base, int off, const Frag& f, int words) {

@@ -91,6 +91,7 @@ struct BackChain {
   float sc[4], el;
   uint32_t v[4][4];
   const uint16_t *ring, *ring_t;   // + this lane's place, plain and for a transpose
+  uint16_t* low;   // f32: the second planes of KF, QT and KT
   // the parts of dS and Y through LDS to wide stores: 563 us against 603 for 8192 tokens of 80 heads of 128 x 128, 89
   // against 87 for 2048 tokens of 96 heads of 64 x 64
   static constexpr bool KEEP = RING && KP == 128;
@@ -144,6 +145,12 @@ struct BackChain {
     load_t(p, w, c);
     load(qt, p.w.QT + group(w, c), w.lane);
     load(kt, p.w.KT + group(w, c), w.lane);
+    load_low(0, p.w.KF + group(w, c), w.lane);
+    load_low(1, p.w.QT + group(w, c), w.lane);
+    load_low(2, p.w.KT + group(w, c), w.lane);
+  }
+  __device__ __forceinline__ void load_low(int i, const uint16_t* base, int lane) {
+    if constexpr (NP == 2) copy_low<NF>(low + i * (NF * kFrag), base + NF * kFrag, lane);
   }
   // One chunk.  soc: the head's scale, 0 in columns behind d_v; s: [4][64] floats of the wave.
   __device__ __forceinline__ void step(const BwdArgs& p, const Place& w, int64_t c, float soc, float rso, float rps, float (*s)[kC]) {
@@ -157,6 +164,7 @@ struct BackChain {
     mscan::wave_lds_sync();
     const float elc = el;
     load_sc(p, w, next);
+    if constexpr (NP == 2) wait_low();
     f32x4 dU[4] = {zero, zero, zero, zero}, pd[4] = {zero, zero, zero, zero}, dO[4];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -169,10 +177,11 @@ struct BackChain {
       for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(get(kf, R::KF, mt * KS + ks), f.lo, dU[mt]);
       if (NP == 2) {
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(at<h8>(KF + group(w, c) + (NF + mt * KS + ks) * kFrag, w.lane * 16), f.hi, dU[mt]);
+        for (int mt = 0; mt < 4; ++mt) dU[mt] = mma(ld8(low + (mt * KS + ks) * kFrag + w.lane * 8), f.hi, dU[mt]);
       }
     }
     load(kf, KF + group(w, next), w.lane);
+    load_low(0, KF + group(w, next), w.lane);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -207,8 +216,9 @@ struct BackChain {
     const Frag e0 = to_b(dO[0], dO[1]), e1 = to_b(dO[2], dO[3]);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) dS[mt] *= elc;
-    update(qt, R::QF, QT + group(w, c), e0, e1, w.lane);
+    update(qt, R::QF, 1, e0, e1, w.lane);
     load(qt, QT + group(w, next), w.lane);
+    load_low(1, QT + group(w, next), w.lane);
     if constexpr (KEEP) {
       const int off = store_off(w.lane, VP), v0 = w.col - w.r;
       mscan::wave_lds_sync();
@@ -231,13 +241,14 @@ struct BackChain {
       dv[mt] = Y[mt] * *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * w.g) * rso;
       Y[mt] *= -*reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * w.g);
     }
-    update(kt, R::KF, KT + group(w, c), to_b(Y[0], Y[1]), to_b(Y[2], Y[3]), w.lane);
+    update(kt, R::KF, 2, to_b(Y[0], Y[1]), to_b(Y[2], Y[3]), w.lane);
     load(kt, KT + group(w, next), w.lane);
+    load_low(2, KT + group(w, next), w.lane);
     store_cols<A>(dv, static_cast<char*>(p.d_v) + w.at_chunk(c), w.row, w.col * Place::ES, w.T - c * kC, w.g, w.ok);
   }
-  // dS += X^T (a, b): X's transposed fragments; f32 inputs have a second plane in global memory
+  // dS += X^T (a, b): X's transposed fragments; f32 inputs have a second plane, `second` of `low`
   template <int N>
-  __device__ __forceinline__ void update(const h8 (&x)[N], int base, const uint16_t* global, const Frag& a, const Frag& b, int lane) {
+  __device__ __forceinline__ void update(const h8 (&x)[N], int base, int second, const Frag& a, const Frag& b, int lane) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) dS[mt] = mma(get_t(x, base, 2 * mt), a.hi, dS[mt]);
 #pragma unroll
@@ -249,8 +260,8 @@ struct BackChain {
     if (NP == 2) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        dS[mt] = mma(at<h8>(global + (NF + 2 * mt) * kFrag, lane * 16), a.hi, dS[mt]);
-        dS[mt] = mma(at<h8>(global + (NF + 2 * mt + 1) * kFrag, lane * 16), b.hi, dS[mt]);
+        dS[mt] = mma(ld8(low + (second * NF + 2 * mt) * kFrag + lane * 8), a.hi, dS[mt]);
+        dS[mt] = mma(ld8(low + (second * NF + 2 * mt + 1) * kFrag + lane * 8), b.hi, dS[mt]);
       }
     }
   }
@@ -261,7 +272,9 @@ __global__ void __launch_bounds__(64) gdelta_bwd_state_kernel(const BwdArgs p) {
   __shared__ __attribute__((aligned(16))) float s[4][kC];   // beta; beta e rk; exp(G_63 - G) rk; e rq
   const PassPlace<A> w(p.d);
   const float so = p.so[w.bh], rso = 1.0f / so, rps = 1.0f / p.d.pscale, soc = w.ok ? so : 0.0f;
+  __shared__ __attribute__((aligned(16))) uint16_t low[3][KP / 8 * kFrag];
   BackChain<A, KP, false> ch;
+  ch.low = low[0];
   ch.init(p, w);
   for (int64_t c = p.d.nc - 1; c >= 0; --c) ch.step(p, w, c, soc, rso, rps, s);
 }

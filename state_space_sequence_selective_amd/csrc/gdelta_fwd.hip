@@ -388,6 +388,7 @@ struct Chain {
   float sc[3], el;
   uint32_t v[4][4];
   const uint16_t *ring, *ring_t;   // + this lane's place, plain and for a transpose
+  uint16_t* low;   // f32: the second planes of KF and KT
 
   template <int N>
   __device__ __forceinline__ h8 get(const h8 (&x)[N], int base, int i) const {
@@ -433,6 +434,11 @@ struct Chain {
     load_t(p, w, 0);
     load_v(p, w, 0);
     load(kt, KT(p, w, 0), w.lane);
+    load_low(0, KF(p, w, 0), w.lane);
+    load_low(1, KT(p, w, 0), w.lane);
+  }
+  __device__ __forceinline__ void load_low(int i, const uint16_t* base, int lane) {
+    if constexpr (NP == 2) copy_low<NF>(low + i * (NF * kFrag), base + NF * kFrag, lane);
   }
   // One chunk.  on_state(step, parts) for the entering state, on_u(parts, parts) for u.  s: [3][64] floats of the wave.
   template <class OnState, class OnU>
@@ -445,6 +451,7 @@ struct Chain {
     mscan::wave_lds_sync();
     const float elc = el;
     load_sc(p, w, next, sv);
+    if constexpr (NP == 2) wait_low();
     f32x4 x[4] = {zero, zero, zero, zero};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -455,11 +462,12 @@ struct Chain {
       for (int mt = 0; mt < 4; ++mt) x[mt] = mma(get(kf, R::KF, mt * KS + ks), f.lo, x[mt]);
       if (NP == 2) {
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) x[mt] = mma(at<h8>(KF(p, w, c) + (NF + mt * KS + ks) * kFrag, w.lane * 16), f.hi, x[mt]);
+        for (int mt = 0; mt < 4; ++mt) x[mt] = mma(ld8(low + (mt * KS + ks) * kFrag + w.lane * 8), f.hi, x[mt]);
       }
       on_state(ks, f);
     }
     load(kf, KF(p, w, next), w.lane);
+    load_low(0, KF(p, w, next), w.lane);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
       const f32x4 be = *reinterpret_cast<const f32x4*>(s[0] + 16 * mt + 4 * w.g), bk = *reinterpret_cast<const f32x4*>(s[1] + 16 * mt + 4 * w.g);
@@ -493,11 +501,12 @@ struct Chain {
     if (NP == 2) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        S[mt] = mma(at<h8>(KT(p, w, c) + (NF + 2 * mt) * kFrag, w.lane * 16), d0.hi, S[mt]);
-        S[mt] = mma(at<h8>(KT(p, w, c) + (NF + 2 * mt + 1) * kFrag, w.lane * 16), d1.hi, S[mt]);
+        S[mt] = mma(ld8(low + (NF + 2 * mt) * kFrag + w.lane * 8), d0.hi, S[mt]);
+        S[mt] = mma(ld8(low + (NF + 2 * mt + 1) * kFrag + w.lane * 8), d1.hi, S[mt]);
       }
     }
     load(kt, KT(p, w, next), w.lane);
+    load_low(1, KT(p, w, next), w.lane);
     on_u(to_b(U[0], U[1]), to_b(U[2], U[3]));
   }
   __device__ __forceinline__ void finish(const FwdArgs& p, const Place& w, float rsv) const {
@@ -523,6 +532,7 @@ struct Output {
   // of 80 heads of 128 x 128 659 against 561
   static constexpr bool KEEP = SAVE && RING && KP == 64;
   uint16_t* kept;   // [KS][high, low] fragments of the wave's own
+  uint16_t* low;    // f32: the second plane of QF
 
   template <int N>
   __device__ __forceinline__ h8 get(const h8 (&x)[N], int base, int i) const {
@@ -534,12 +544,14 @@ struct Output {
   __device__ __forceinline__ const uint16_t* P(const FwdArgs& p, const Place& w, int64_t c) const { return p.w.P + (w.bh * w.nc + c) * (PP * 6 * kFrag); }
   __device__ __forceinline__ void load_q(const FwdArgs& p, const Place& w, int64_t c) {
     if constexpr (!RING) load_frags(qf, QF(p, w, c), w.lane);
+    if constexpr (NP == 2) copy_low<NF>(low, QF(p, w, c) + NF * kFrag, w.lane);
     eq = p.w.hsc[(w.bh * w.nc + c) * (kHeadSc * kC) + H_EQ * kC + w.lane] * p.d.pscale;
   }
   __device__ __forceinline__ void load_p(const FwdArgs& p, const Place& w, int64_t c) {
     if constexpr (!RING) load_frags(pf, P(p, w, c), w.lane);
   }
   __device__ __forceinline__ void begin(const Place& w, float* s) {
+    if constexpr (NP == 2) wait_low();
     mscan::wave_lds_sync();
     s[w.lane] = eq;
     mscan::wave_lds_sync();
@@ -557,7 +569,7 @@ struct Output {
     }
     if (NP == 2) {
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) y[mt] = mma(at<h8>(QF(p, w, c) + (NF + mt * KS + ks) * kFrag, w.lane * 16), f.hi, y[mt]);
+      for (int mt = 0; mt < 4; ++mt) y[mt] = mma(ld8(low + (mt * KS + ks) * kFrag + w.lane * 8), f.hi, y[mt]);
     }
   }
   __device__ __forceinline__ void u(const FwdArgs& p, const Place& w, int64_t c, float scale, const float* s, const Frag& u0, const Frag& u1) {
@@ -611,6 +623,7 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
   constexpr bool LOW = SAVE || kPPlanes<A> == 2;   // the output takes the low parts too
   __shared__ __attribute__((aligned(16))) float s[4][kC];   // beta sv; beta e rk; exp(G_63 - G) rk / e rq pscale
   const Dims& d = p.d;
+  __shared__ __attribute__((aligned(16))) uint16_t low[3][A == Act::F32 ? KP / 8 * kFrag : 1];
   const PassPlace<A> w(d);
   const float sv = head_scale(p, w.bh, w.lane);
   const float rsv = 1.0f / sv, yscale = rsv / d.pscale;
@@ -619,6 +632,7 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
     __shared__ __attribute__((aligned(16))) PassBuf<KP> buf[2];
     if (wave_id() == 0) {
       Chain<A, KP, false> ch;
+      ch.low = low[0];
       ch.init(p, w, sv);
       for (int64_t c = 0; c < d.nc; ++c) {
         PassBuf<KP>& o = buf[c & 1];
@@ -640,6 +654,7 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
       ch.finish(p, w, rsv);
     } else {
       Output<A, KP, SAVE, false> out;
+      out.low = low[2];
       out.load_q(p, w, 0);
       out.load_p(p, w, 0);
       for (int64_t c = 0; c < d.nc; ++c) {
@@ -666,6 +681,8 @@ __global__ void __launch_bounds__(PAIR ? 128 : 64) gdelta_fwd_kernel(const FwdAr
   } else {
     Chain<A, KP, false> ch;
     Output<A, KP, SAVE, false> out;
+    ch.low = low[0];
+    out.low = low[2];
     ch.init(p, w, sv);
     out.load_q(p, w, 0);
     out.load_p(p, w, 0);
