@@ -887,7 +887,7 @@ hipError_t launch_chunks(const FwdArgs& a, bool save, hipStream_t st) {
   hipLaunchKernelGGL((gdelta_prep_kernel<A, KP>), dim3(bh * nc), dim3(256), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const unsigned tiles = bh * (d.VP / 16);
-  if (tiles <= (save ? kPairTilesSave : kPairTiles)) {
+  if (tiles <= (save && A != Act::F32 ? kPairTilesSave : kPairTiles)) {
     if (save) hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, true, true>), dim3(tiles), dim3(128), 0, st, a);
     else hipLaunchKernelGGL((gdelta_fwd_kernel<A, KP, false, true>), dim3(tiles), dim3(128), 0, st, a);
   } else if constexpr (A == Act::F32) {   // two planes a family: a chunk's fragments twice are more than the LDS

@@ -8,9 +8,10 @@
 namespace gdelta {
 
 // How the forward pass over the chunks has its 16-column tiles: up to kPairTiles of them (kPairTilesSave with what a backward
-// pass reads) each has two waves of its own; more share their chunks' fragments in LDS.  Forwards of 2048 tokens, 128 x
-// 128, bf16: 155 us against 186 at 64 heads (512 tiles), 249 against 217 at 80; training passes 318 against 330 at 32
-// heads (256 tiles), 408 and 403 at 40, 574 and 558 at 64.
+// pass reads, 16-bit inputs) each has two waves of its own; more share their chunks' fragments in LDS, or, f32 inputs, have
+// one wave each.  2048 tokens of 128 x 128: bf16 forwards 155 us against 186 at 64 heads (512 tiles), 249 against 217 at
+// 80; bf16 training passes 318 against 330 at 32 heads (256 tiles), 408 and 403 at 40, 574 and 558 at 64; f32 forwards 305
+// against 395 at 64 heads, 541 and 514 at 96, training passes 972 and 1076, 1447 and 1429.
 constexpr unsigned kPairTiles = 512, kPairTilesSave = 256;
 
 // Tiles of a workgroup that shares its fragments in LDS (it fills a CU): 3 where that takes no more rounds over the 256 CUs
