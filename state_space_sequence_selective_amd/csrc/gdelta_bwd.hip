@@ -74,8 +74,9 @@ __global__ void __launch_bounds__(64) gdelta_dscale_kernel(const BwdArgs p) {
 
 // ------------------------------------------------------------------ pass from the last chunk to the first
 // As the forward's pass: a wave holds 16 columns of dS^T and needs nothing of any other, but for the fragments that the
-// tiles of a head share; they come a chunk ahead, to LDS for 16-bit inputs (two planes of f32 inputs twice are more than
-// it holds: registers).  Fragments of a chunk in the shared buffer, in this order:
+// tiles of a head share; they come a chunk ahead, to LDS for 16-bit inputs; f32 inputs have two planes, twice of which are
+// more than it holds: each wave has the first in registers, the second in LDS.  Fragments of a chunk in the shared buffer,
+// in this order:
 template <int KP>
 struct BwdRing {
   static constexpr int NF = KP / 8, KF = 0, PT = NF, TT = PT + 12, QF = TT + 12, N = QF + NF;
